@@ -69,7 +69,7 @@ typedef enum qlora_status {
 typedef enum qlora_dtype { QLORA_F32 = 0, QLORA_BF16 = 1 } qlora_dtype;
 
 /* Operation whose workspace size qlora_workspace_bytes() reports. */
-typedef enum qlora_op { QLORA_OP_FWD = 1, QLORA_OP_BWD = 2 } qlora_op;
+typedef enum qlora_op { QLORA_OP_FWD = 1, QLORA_OP_BWD = 2, QLORA_OP_MATVEC = 3 } qlora_op;
 
 /* Fixed format constants. */
 #define QLORA_BLOCK 64   /* weights per absmax block */
@@ -302,15 +302,52 @@ QLORA_API qlora_status qlora_linear_bwd(const qlora_nf4_weight* w, const uint16_
  *                  it, e.g. Bernoulli(1 - p), and keeps it).  Read only.
  *   dropout_p      the drop probability p in [0, 1) the kept values are rescaled
  *                  by; checked only with a mask, else QLORA_ERR_INVALID_ARG.
+ *                  QLORA_DROPOUT_COUNTER: the same dropout with the mask of
+ *                  qlora_dropout_mask(dropout, M, r), formed where V and U are
+ *                  stored and never written out: the same bits as with those bytes
+ *                  in dropout_keep.  dropout_keep must then be NULL
+ *                  (QLORA_ERR_INVALID_ARG otherwise) and dropout_p is not read.
+ *   dropout        read only with QLORA_DROPOUT_COUNTER (a caller built against the
+ *                  options without this member never sets that flag).
  * A NULL options pointer means adapter_scale = 1, no flags and no dropout.
  */
 #define QLORA_ACCUMULATE_GRADS 1u
+#define QLORA_DROPOUT_COUNTER 2u
+
+/*
+ * Dropout from a counter-based generator: the mask is a function of these numbers
+ * and the element's place, so the forward and the backward form the same one and
+ * nothing is stored.  Element e (row-major) of a tensor takes word e mod 4 of
+ * Philox4x32-10 (Salmon, Moraes, Dror, Shaw 2011) at the counter
+ * (lo32(e / 4), hi32(e / 4), lo32(off), hi32(off)) under the key
+ * (lo32(seed), hi32(seed)), off = offset + *counter (mod 2^64); it is kept where
+ * the word is >= rint(p 2^32), and a kept value is multiplied by fl32(1 / (1 - p)).
+ *   p        drop probability in [0, 1), else QLORA_ERR_INVALID_ARG; 0 drops nothing.
+ *   seed     one per use (layer, call site); equal seeds and offsets give equal masks.
+ *   offset   one per step: the forward's and backward's must agree.
+ *   counter  [device] one 64-bit value added to offset, 8-byte aligned, or NULL: a
+ *            captured CUDA graph keeps offset as it was, so a replay that shall draw
+ *            anew reads its step number from here.
+ */
+typedef struct {
+  float p;
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* counter;
+} qlora_dropout;
+
 typedef struct {
   float adapter_scale;
   uint32_t flags;
   const uint8_t* dropout_keep;
   float dropout_p;
+  qlora_dropout dropout;
 } qlora_linear_opts;
+
+/* The mask of `d` for a row-major (M, n) tensor as bytes, 1 = keep.
+ *   keep  [device] out: uint8 (M, n).
+ * QLORA_ERR_SHAPE unless 1 <= M, 1 <= n and M n <= 2^40. */
+QLORA_API qlora_status qlora_dropout_mask(const qlora_dropout* d, int64_t M, int64_t n, uint8_t* keep, void* stream);
 
 /* qlora_linear_fwd with options (arguments otherwise as there). */
 QLORA_API qlora_status qlora_linear_fwd_ex(const qlora_nf4_weight* w, const uint16_t* X, int64_t M,
@@ -414,9 +451,88 @@ QLORA_API qlora_status qlora_loftq_split(const float* U, int64_t ldu, const floa
                                          int64_t ldv, int64_t in, int64_t out, int r, uint16_t* A,
                                          uint16_t* B, void* stream);
 
+/*
+ * Residual addition and RMS norm, what stands between two adapted linears (the
+ * pages adapt "all linear layers" of a decoder and leave the rest to the model):
+ *   h = bf16(R + keep X fl32(1 / (1 - p)))      (bf16(R + X) without dropout, X without both)
+ *   rstd = 1 / sqrt(mean_k h_k^2 + eps),  y_k = h_k rstd G_k
+ * with the squares summed and y formed in fp32.
+ *   X        [device] bf16 (M, n), the branch's output.
+ *   R        [device] bf16 (M, n), the residual stream, or NULL for none.
+ *   G        [device] the gain, n values of g_dtype (QLORA_F32 or QLORA_BF16).
+ *   eps      > 0 and finite, else QLORA_ERR_INVALID_ARG.
+ *   drop     [host] dropout of X (mask over (M, n)), or NULL.
+ *   H        [device] out: bf16 (M, n), or NULL where it is not wanted.
+ *   Y        [device] out: bf16(y) (M, n), or NULL.
+ *   Q        [device] out: y in 8 bits, uint8 (M, n) E4M3 codes, or NULL.  Per block
+ *            of q_block columns (64, or 0 for the whole row): a = max |y|,
+ *            s = fl32(a / 448), code = E4M3(fl32(y / s)) round to nearest even (0
+ *            where s = 0), so y ~ code s.  y is not rounded to bf16 in between.  A
+ *            block that holds a NaN or an infinity gets codes and a scale whose
+ *            products are NaN.
+ *   q_scales [device] out: fp32 (M, n / 64), or (M) with q_block = 0.  With Q only.
+ *   rstd     [device] out: fp32 (M), for the backward, or NULL.
+ * QLORA_ERR_INVALID_ARG without Y and Q, with Q but no q_scales, or for another q_block.
+ * QLORA_ERR_SHAPE unless M >= 1, n % 8 == 0 and 8 <= n <= 65536 (n % 64 == 0 with q_block = 64).
+ */
+QLORA_API qlora_status qlora_rmsnorm_fwd(const uint16_t* X, const uint16_t* R, const void* G, int g_dtype, float eps,
+                                         int64_t M, int64_t n, const qlora_dropout* drop, uint16_t* H, uint16_t* Y,
+                                         uint8_t* Q, float* q_scales, int q_block, float* rstd, void* stream);
+
+/*
+ * Gradient of the call above (through y; the 8-bit output has none of its own).
+ *   gh = G dY,  c = mean_k(gh_k h_k) rstd^2,  dh = rstd (gh - h c) + dH
+ *   dR = bf16(dh),  dX = bf16(keep dh fl32(1 / (1 - p))),  dG = sum over rows of dY h rstd
+ *   dY    [device] bf16 (M, n).   H [device] bf16 (M, n): the forward's h (its X
+ *         where it had neither R nor dropout).   rstd [device] fp32 (M), the forward's.
+ *   dH    [device] bf16 (M, n): what reaches h past the norm (the residual stream's
+ *         gradient), or NULL.
+ *   drop  [host] the forward's, or NULL.
+ *   dR    [device] out: bf16 (M, n), the gradient of R, and of X without dropout.
+ *   dX    [device] out: bf16 (M, n), the gradient of X under dropout, or NULL.
+ *         QLORA_ERR_INVALID_ARG if given without dropout (p = 0 is none).
+ *   dG    [device] out: fp32 (n), or NULL where the gain is frozen.
+ *   flags QLORA_ACCUMULATE_GRADS adds dG to what is there.
+ *   ws    [device] at least qlora_rmsnorm_ws_bytes(M, n) bytes, initialised by
+ *         qlora_ws_init (it may be the layer's); needed with dG only.
+ * The sums have a fixed order: equal inputs give equal bits.
+ */
+QLORA_API qlora_status qlora_rmsnorm_bwd(const uint16_t* dY, const uint16_t* H, const void* G, int g_dtype,
+                                         const float* rstd, const uint16_t* dH, int64_t M, int64_t n,
+                                         const qlora_dropout* drop, uint16_t* dR, uint16_t* dX, float* dG,
+                                         uint32_t flags, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of qlora_rmsnorm_bwd with dG (0 for invalid sizes).  Host only. */
+QLORA_API size_t qlora_rmsnorm_ws_bytes(int64_t M, int64_t n);
+
+/*
+ * A few tokens through an integer weight (dq_format QLORA_FMT_INT16: 4-bit codes,
+ * one scale per 16 weights), with or without adapters -- the decode step of a
+ * layer on that base, at the speed of reading the weight once:
+ *   V = bf16(s X A),   Y = bf16(X w' + V B),   w' = (code - 8) scale
+ * with fp32 accumulation; unlike qlora_linear_fwd it does not round w' to bf16 and
+ * it reads 8-bit activations as qlora_rmsnorm_fwd writes them.
+ *   w         [host] descriptor; another format is QLORA_ERR_INVALID_ARG.
+ *   X         [device] bf16 (M, in), or with x_scales uint8 (M, in) E4M3 codes.
+ *   x_scales  [device] fp32 (M, in / 64) for x_block = 64, (M) for x_block = 0:
+ *             x = code scale; or NULL for bf16 X (x_block is then not read).
+ *   A, B      [device] bf16 (in, r) and (r, out); both NULL with r = 0 (no adapter).
+ *   r         0, or 8 <= r <= 256 with r % 8 == 0.
+ *   s         adapter_scale, finite.
+ *   Y         [device] out: bf16 (M, out).
+ *   V_save    [device] out: bf16 (M, r), or NULL (V then lives in the workspace).
+ *   ws        [device] at least qlora_workspace_bytes(QLORA_OP_MATVEC, ...) bytes,
+ *             initialised by qlora_ws_init (it may be the layer's).
+ * QLORA_ERR_SHAPE unless 1 <= M <= 16, in % 64 == 0 and out % 64 == 0.
+ */
+QLORA_API qlora_status qlora_matvec(const qlora_nf4_weight* w, const void* X, const float* x_scales, int x_block,
+                                    int64_t M, const uint16_t* A, const uint16_t* B, int r, float adapter_scale,
+                                    uint16_t* Y, uint16_t* V_save, void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- helpers */
 
-/* Bytes of workspace qlora_linear_fwd / qlora_linear_bwd use at these sizes on
+/* Bytes of workspace qlora_linear_fwd / qlora_linear_bwd / qlora_matvec
+ * (QLORA_OP_MATVEC: the prefix and V, r = 0 allowed) use at these sizes on
  * the current device (0 for an unknown op or invalid sizes).  Host only: it reads
  * the device's SM count, no device memory.
  * Layout: a 1280-byte prefix (the 256-byte status word, then 1 KB of counters
@@ -466,7 +582,10 @@ typedef enum qlora_kernel {
   QLORA_KERNEL_FWD_GEMM = 4,   /* fused dequant GEMM of the forward */
   QLORA_KERNEL_DX_GEMM = 5,    /* fused dequant GEMM of dX */
   QLORA_KERNEL_RANK_R = 6,     /* the rank-r kernels: V, U, dA, dB (and their split sums) */
-  QLORA_KERNEL_GEMV = 7        /* small-M forward (M <= 16) */
+  QLORA_KERNEL_GEMV = 7,       /* small-M forward (M <= 16) */
+  QLORA_KERNEL_MATVEC = 8,     /* few tokens through an integer weight (qlora_matvec) */
+  QLORA_KERNEL_RMSNORM = 9,    /* qlora_rmsnorm_fwd */
+  QLORA_KERNEL_RMSNORM_BWD = 10 /* qlora_rmsnorm_bwd, the gain's reduction included */
 } qlora_kernel;
 
 /* Arm launch timing for benchmarks: the next n launches of kernel `which` are

@@ -22,8 +22,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqlora.so")
 
 QLORA_F32, QLORA_BF16 = 0, 1
-QLORA_OP_FWD, QLORA_OP_BWD = 1, 2
+QLORA_OP_FWD, QLORA_OP_BWD, QLORA_OP_MATVEC = 1, 2, 3
 BLOCK, GROUP = 64, 256
+_WS_PREFIX = 1280   # bytes of a workspace that every call needs
 
 STATUS_NAMES = {
     0: "QLORA_OK", 1: "QLORA_ERR_INVALID_ARG", 2: "QLORA_ERR_SHAPE", 3: "QLORA_ERR_ALIGNMENT",
@@ -39,19 +40,20 @@ EXPORTS = (
     "qlora_linear_fwd_static_ws", "qlora_linear_bwd_adam", "qlora_linear_fwd_ex", "qlora_linear_bwd_ex",
     "qlora_gemm_set_ctas", "qlora_quantize_nf4_ex", "qlora_quantize_int", "qlora_dequantize_int",
     "qlora_static_ws_status", "qlora_quantize_status", "qlora_selftest_wait_timeout",
-    "qlora_loftq_residual", "qlora_loftq_split", "qlora_quantize_nf4_batch",
+    "qlora_loftq_residual", "qlora_loftq_split", "qlora_quantize_nf4_batch", "qlora_dropout_mask",
+    "qlora_rmsnorm_fwd", "qlora_rmsnorm_bwd", "qlora_rmsnorm_ws_bytes", "qlora_matvec",
 )
 
 # Weight formats (NF4Weight.dq_format): NF4 with E4M3 or linear uint8 absmax
 # codes, or the symmetric INT format of qlora_quantize_int (one scale per 16).
 QLORA_DQ_E4M3, QLORA_DQ_U8, QLORA_FMT_INT16 = 0, 1, 2
 
-# Flag of qlora_linear_opts.flags.
-QLORA_ACCUMULATE_GRADS = 1
+# Flags of qlora_linear_opts.flags.
+QLORA_ACCUMULATE_GRADS, QLORA_DROPOUT_COUNTER = 1, 2
 
 # Kernel ids of qlora_time_kernel.
 KERNEL_QUANTIZE, KERNEL_DEQUANTIZE, KERNEL_MERGE, KERNEL_FWD_GEMM, KERNEL_DX_GEMM, KERNEL_RANK_R = 1, 2, 3, 4, 5, 6
-KERNEL_GEMV = 7
+KERNEL_GEMV, KERNEL_MATVEC, KERNEL_RMSNORM, KERNEL_RMSNORM_BWD = 7, 8, 9, 10
 
 
 class QLoRAError(RuntimeError):
@@ -75,9 +77,14 @@ class _AdamHparams(ctypes.Structure):
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("step", ctypes.c_int64)]
 
 
+class _Dropout(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("counter", ctypes.c_void_p)]
+
+
 class _LinearOpts(ctypes.Structure):
     _fields_ = [("adapter_scale", ctypes.c_float), ("flags", ctypes.c_uint32),
-                ("dropout_keep", ctypes.c_void_p), ("dropout_p", ctypes.c_float)]
+                ("dropout_keep", ctypes.c_void_p), ("dropout_p", ctypes.c_float), ("dropout", _Dropout)]
 
 
 class _AdamState(ctypes.Structure):
@@ -95,7 +102,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: run `python -m quantized_rank_fine_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
-        wp = ctypes.POINTER(_Weight)
+        wp, dp, f32, u32 = ctypes.POINTER(_Weight), ctypes.POINTER(_Dropout), ctypes.c_float, ctypes.c_uint32
         sig = {
             "qlora_quantize_nf4": (i32, [vp, i64, i64, vp, vp, vp, vp]),
             "qlora_dequantize": (i32, [wp, vp, i32, vp]),
@@ -124,6 +131,11 @@ def lib() -> ctypes.CDLL:
             "qlora_linear_bwd_adam": (i32, [wp, vp, vp, vp, i64, vp, vp, i32, vp, ctypes.POINTER(_AdamState),
                                             ctypes.POINTER(_AdamHparams), ctypes.POINTER(_LinearOpts), vp, sz,
                                             vp]),
+            "qlora_dropout_mask": (i32, [dp, i64, i64, vp, vp]),
+            "qlora_rmsnorm_fwd": (i32, [vp, vp, vp, i32, f32, i64, i64, dp, vp, vp, vp, vp, i32, vp, vp]),
+            "qlora_rmsnorm_bwd": (i32, [vp, vp, vp, i32, vp, vp, i64, i64, dp, vp, vp, vp, u32, vp, sz, vp]),
+            "qlora_rmsnorm_ws_bytes": (sz, [i64, i64]),
+            "qlora_matvec": (i32, [wp, vp, vp, i32, i64, vp, vp, i32, f32, vp, vp, vp, sz, vp]),
             "qlora_linear_fwd_ex": (i32, [wp, vp, i64, vp, vp, i32, vp, vp, ctypes.POINTER(_LinearOpts), vp, sz,
                                           vp]),
             "qlora_linear_bwd_ex": (i32, [wp, vp, vp, vp, i64, vp, vp, i32, vp, vp, vp,
@@ -149,6 +161,20 @@ def _ptr(t):
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
     return t.data_ptr()
+
+
+def _empty(shape, dtype, device, stream=None):
+    """A new tensor whose memory belongs to the stream the call runs on."""
+    if stream is None or not isinstance(stream, torch.cuda.Stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _is(t, shape, *dtypes):
+    """Refuse a tensor of another shape or type: the C calls see pointers only."""
+    if t is not None and (t.dtype not in dtypes or t.shape != shape):
+        raise ValueError(f"expected {tuple(shape)} of {' or '.join(map(str, dtypes))}, got {tuple(t.shape)} of {t.dtype}")
 
 
 def _stream(stream=None):
@@ -357,9 +383,48 @@ def qlora_merge(w: NF4Weight, A: torch.Tensor, B: torch.Tensor, dtype=torch.floa
     return out
 
 
-def _opts(adapter_scale: float, accumulate: bool = False, dropout_keep=None, dropout_p: float = 0.0):
-    return _LinearOpts(adapter_scale, QLORA_ACCUMULATE_GRADS if accumulate else 0,
-                       _ptr(dropout_keep) if dropout_keep is not None else None, dropout_p)
+@dataclass
+class Dropout:
+    """Dropout from the counter-based generator: the mask follows from these
+    numbers and each element's place and is never stored.  `seed` names the call
+    site, `offset` the step (the same pair in the forward and the backward);
+    `counter`, an int64 device tensor of one element, is added to offset when the
+    kernel runs, so that a captured graph can draw anew at every replay."""
+    p: float
+    seed: int
+    offset: int = 0
+    counter: torch.Tensor | None = None
+
+    def c_struct(self) -> _Dropout:
+        c = self.counter
+        if c is not None and (c.dtype != torch.int64 or c.numel() != 1):
+            raise ValueError("counter must be one int64")
+        if not 0 <= self.seed < 1 << 64 or not 0 <= self.offset < 1 << 64:
+            raise ValueError("seed and offset must lie in [0, 2^64)")
+        return _Dropout(self.p, self.seed, self.offset, _ptr(c))
+
+
+def _drop(dropout):
+    """The C argument of an optional Dropout (None without one, or with p = 0)."""
+    return None if dropout is None or dropout.p == 0.0 else ctypes.byref(dropout.c_struct())
+
+
+def _opts(adapter_scale: float, accumulate: bool = False, dropout_keep=None, dropout_p: float = 0.0, dropout=None):
+    flags = QLORA_ACCUMULATE_GRADS if accumulate else 0
+    if dropout is not None:
+        flags |= QLORA_DROPOUT_COUNTER
+    return _LinearOpts(adapter_scale, flags, _ptr(dropout_keep) if dropout_keep is not None else None, dropout_p,
+                       _Dropout() if dropout is None else dropout.c_struct())
+
+
+def qlora_dropout_mask(M: int, n: int, dropout: Dropout, device="cuda", stream=None, out=None) -> torch.Tensor:
+    """The mask that `dropout` stands for on an (M, n) tensor: uint8, 1 = keep.
+    Passed as dropout_keep it gives the same bits as the Dropout itself."""
+    if out is None:
+        out = _empty((M, n), torch.uint8, torch.device(device), stream)
+    d = dropout.c_struct()
+    _check(lib().qlora_dropout_mask(ctypes.byref(d), M, n, _ptr(out), _stream(stream)), "qlora_dropout_mask")
+    return out
 
 
 def dropout_mask(M: int, r: int, p: float, generator=None, device="cuda") -> torch.Tensor:
@@ -374,10 +439,11 @@ def dropout_mask(M: int, r: int, p: float, generator=None, device="cuda") -> tor
 
 def qlora_linear_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, workspace: Workspace,
                      save_V: bool = True, stream=None, Y=None, V=None, adapter_scale: float = 1.0,
-                     dropout_keep=None, dropout_p: float = 0.0):
+                     dropout_keep=None, dropout_p: float = 0.0, dropout: Dropout | None = None):
     """Returns (Y, V) with V = s X A (None when save_V is False); s =
     adapter_scale (alpha / r), 1 for the plain layer.  With dropout_keep (uint8
-    (M, r) on the device, 1 = keep) V is dropped out: s (X A) keep / (1 - p)."""
+    (M, r) on the device, 1 = keep) V is dropped out: s (X A) keep / (1 - p); with
+    `dropout` the mask comes from the generator and is not stored."""
     M, r = X.shape[0], A.shape[1]
     if Y is None:
         Y = torch.empty((M, w.n_out), dtype=torch.bfloat16, device=X.device)
@@ -386,12 +452,12 @@ def qlora_linear_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Te
     nb = qlora_workspace_bytes(QLORA_OP_FWD, M, w.n_in, w.n_out, r)
     buf = workspace.get(nb, stream)
     ws = w.c_struct()
-    if adapter_scale == 1.0 and dropout_keep is None:
+    if adapter_scale == 1.0 and dropout_keep is None and dropout is None:
         _check(lib().qlora_linear_fwd(ctypes.byref(ws), _ptr(X), M, _ptr(A), _ptr(B), r, _ptr(Y),
                                       _ptr(V) if save_V else None, _ptr(buf), buf.numel(), _stream(stream)),
                "qlora_linear_fwd")
     else:
-        o = _opts(adapter_scale, False, dropout_keep, dropout_p)
+        o = _opts(adapter_scale, False, dropout_keep, dropout_p, dropout)
         _check(lib().qlora_linear_fwd_ex(ctypes.byref(ws), _ptr(X), M, _ptr(A), _ptr(B), r, _ptr(Y),
                                          _ptr(V) if save_V else None, ctypes.byref(o), _ptr(buf), buf.numel(),
                                          _stream(stream)), "qlora_linear_fwd_ex")
@@ -401,10 +467,10 @@ def qlora_linear_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Te
 def qlora_linear_bwd(w: NF4Weight, X: torch.Tensor, V, dY: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                      workspace: Workspace, need_dX: bool = True, stream=None, dX=None, dA=None, dB=None,
                      adapter_scale: float = 1.0, accumulate: bool = False, dropout_keep=None,
-                     dropout_p: float = 0.0):
+                     dropout_p: float = 0.0, dropout: Dropout | None = None):
     """Returns (dX or None, dA fp32 (in, r), dB fp32 (r, out)).  With accumulate,
     dA and dB (given) receive the sums instead of being overwritten.  Under
-    dropout pass the forward's mask and p."""
+    dropout pass the forward's mask and p, or its Dropout."""
     if accumulate and (dA is None or dB is None):
         raise ValueError("accumulate needs the dA and dB to add into")
     M, r = X.shape[0], A.shape[1]
@@ -418,12 +484,12 @@ def qlora_linear_bwd(w: NF4Weight, X: torch.Tensor, V, dY: torch.Tensor, A: torc
     nb = qlora_workspace_bytes(QLORA_OP_BWD, M, w.n_in, w.n_out, r)
     buf = workspace.get(nb, stream)
     ws = w.c_struct()
-    if adapter_scale == 1.0 and not accumulate and dropout_keep is None:
+    if adapter_scale == 1.0 and not accumulate and dropout_keep is None and dropout is None:
         _check(lib().qlora_linear_bwd(ctypes.byref(ws), _ptr(X), _ptr(V), _ptr(dY), M, _ptr(A), _ptr(B), r,
                                       _ptr(dX) if need_dX else None, _ptr(dA), _ptr(dB), _ptr(buf), buf.numel(),
                                       _stream(stream)), "qlora_linear_bwd")
     else:
-        o = _opts(adapter_scale, accumulate, dropout_keep, dropout_p)
+        o = _opts(adapter_scale, accumulate, dropout_keep, dropout_p, dropout)
         _check(lib().qlora_linear_bwd_ex(ctypes.byref(ws), _ptr(X), _ptr(V), _ptr(dY), M, _ptr(A), _ptr(B), r,
                                          _ptr(dX) if need_dX else None, _ptr(dA), _ptr(dB), ctypes.byref(o),
                                          _ptr(buf), buf.numel(), _stream(stream)), "qlora_linear_bwd_ex")
@@ -444,7 +510,7 @@ def qlora_linear_bwd_adam(w: NF4Weight, X: torch.Tensor, V, dY: torch.Tensor, A:
                           state: dict, step: int, workspace: Workspace, lr: float = 1e-3, beta1: float = 0.9,
                           beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0,
                           need_dX: bool = True, stream=None, dX=None, adapter_scale: float = 1.0,
-                          dropout_keep=None, dropout_p: float = 0.0):
+                          dropout_keep=None, dropout_p: float = 0.0, dropout: Dropout | None = None):
     """Backward with one fused Adam/AdamW step on the adapters: updates `state`
     (fp32 A32, B32, mA, vA, mB, vB) and the bf16 A and B in place; returns dX or None."""
     M, r = X.shape[0], A.shape[1]
@@ -455,12 +521,135 @@ def qlora_linear_bwd_adam(w: NF4Weight, X: torch.Tensor, V, dY: torch.Tensor, A:
     ws = w.c_struct()
     st = _AdamState(*[_ptr(state[k]) for k in ("A32", "B32", "mA", "vA", "mB", "vB")])
     hp = _AdamHparams(lr, beta1, beta2, eps, weight_decay, step)
-    o = _opts(adapter_scale, False, dropout_keep, dropout_p)
+    o = _opts(adapter_scale, False, dropout_keep, dropout_p, dropout)
     _check(lib().qlora_linear_bwd_adam(ctypes.byref(ws), _ptr(X), _ptr(V), _ptr(dY), M, _ptr(A), _ptr(B), r,
                                        _ptr(dX) if need_dX else None, ctypes.byref(st), ctypes.byref(hp),
                                        ctypes.byref(o), _ptr(buf), buf.numel(), _stream(stream)),
            "qlora_linear_bwd_adam")
     return dX if need_dX else None
+
+
+# ---------------------------------------------------------------- around the layer
+
+@dataclass
+class Act8:
+    """Activations in 8 bits: value = code scale, with E4M3 codes and one fp32
+    scale per row (block 0) or per 64 columns (block 64)."""
+    codes: torch.Tensor    # uint8 (M, n)
+    scales: torch.Tensor   # float32 (M, 1) or (M, n / 64)
+    block: int = 0
+
+
+@dataclass
+class RMSNormOut:
+    """What qlora_rmsnorm_fwd wrote; None where a part was not asked for."""
+    H: torch.Tensor | None      # bf16 (M, n): the residual stream after the addition
+    Y: torch.Tensor | None      # bf16 (M, n)
+    act: Act8 | None            # y in 8 bits
+    rstd: torch.Tensor | None   # float32 (M)
+
+
+def _gain_dtype(G, n):
+    _is(G, (n,), torch.float32, torch.bfloat16)
+    return QLORA_F32 if G.dtype == torch.float32 else QLORA_BF16
+
+
+def qlora_rmsnorm_fwd(X: torch.Tensor, G: torch.Tensor, eps: float = 1e-5, residual=None,
+                      dropout: Dropout | None = None, want_y: bool = True, quant_block: int | None = None,
+                      save_rstd: bool = False, stream=None, H=None, Y=None) -> RMSNormOut:
+    """h = residual + dropout(X), y = h rstd G for bf16 (M, n) rows and a gain G in
+    bf16 or fp32.  The result holds H (only with a residual or dropout: else h is X
+    itself), Y = bf16(y) unless want_y is False, y in 8 bits with quant_block 0 (one
+    scale a row) or 64 (one per 64 columns), and rstd for the backward."""
+    M, n = X.shape
+    bf16 = torch.bfloat16
+    for t in (X, residual, H, Y):
+        _is(t, (M, n), bf16)
+    d = _drop(dropout)
+    gd = _gain_dtype(G, n)
+    dev = X.device
+    if H is None and (residual is not None or d is not None):
+        H = _empty((M, n), bf16, dev, stream)
+    if Y is None and want_y:
+        Y = _empty((M, n), bf16, dev, stream)
+    act = None
+    if quant_block is not None:
+        nb = n // quant_block if quant_block > 0 else 1
+        act = Act8(_empty((M, n), torch.uint8, dev, stream), _empty((M, nb), torch.float32, dev, stream), quant_block)
+    rstd = _empty((M,), torch.float32, dev, stream) if save_rstd else None
+    _check(lib().qlora_rmsnorm_fwd(_ptr(X), _ptr(residual), _ptr(G), gd, eps, M, n, d, _ptr(H), _ptr(Y),
+                                   _ptr(act.codes) if act else None, _ptr(act.scales) if act else None,
+                                   quant_block or 0, _ptr(rstd), _stream(stream)), "qlora_rmsnorm_fwd")
+    return RMSNormOut(H, Y, act, rstd)
+
+
+def qlora_rmsnorm_bwd(dY: torch.Tensor, H: torch.Tensor, G: torch.Tensor, rstd: torch.Tensor, workspace: Workspace,
+                      dH=None, dropout: Dropout | None = None, need_dG: bool = True, accumulate: bool = False,
+                      stream=None, dR=None, dX=None, dG=None):
+    """Returns (dX, dR, dG): the gradients of the branch X, of the residual, and of
+    the gain (fp32, None without need_dG).  H is the forward's h (its X where it had
+    neither residual nor dropout), dH the gradient that reaches h past the norm.
+    Without dropout dX is dR.  With accumulate dG (given) receives the sum."""
+    if accumulate and dG is None:
+        raise ValueError("accumulate needs the dG to add into")
+    M, n = H.shape
+    bf16 = torch.bfloat16
+    for t in (dY, H, dH, dR, dX):
+        _is(t, (M, n), bf16)
+    _is(rstd, (M,), torch.float32)
+    _is(dG, (n,), torch.float32)
+    d = _drop(dropout)
+    gd = _gain_dtype(G, n)
+    if dR is None:
+        dR = _empty((M, n), bf16, H.device, stream)
+    if d is None:
+        dX = None
+    elif dX is None:
+        dX = _empty((M, n), bf16, H.device, stream)
+    buf = None
+    if need_dG:
+        if dG is None:
+            dG = _empty((n,), torch.float32, H.device, stream)
+        buf = workspace.get(max(_WS_PREFIX, lib().qlora_rmsnorm_ws_bytes(M, n)), stream)
+    _check(lib().qlora_rmsnorm_bwd(_ptr(dY), _ptr(H), _ptr(G), gd, _ptr(rstd), _ptr(dH), M, n, d, _ptr(dR), _ptr(dX),
+                                   _ptr(dG) if need_dG else None, QLORA_ACCUMULATE_GRADS if accumulate else 0,
+                                   _ptr(buf), buf.numel() if need_dG else 0, _stream(stream)), "qlora_rmsnorm_bwd")
+    return (dR if d is None else dX), dR, (dG if need_dG else None)
+
+
+def qlora_matvec(w: NF4Weight, X, workspace: Workspace, A=None, B=None, adapter_scale: float = 1.0,
+                 save_V: bool = False, stream=None, Y=None, V=None):
+    """Up to 16 tokens through an integer weight (int_weight): X is bf16 (M, in) or
+    the Act8 that qlora_rmsnorm_fwd returns; A and B the adapters, or None.  Returns
+    (Y, V), V = s X A with save_V and adapters, else None."""
+    if isinstance(X, Act8):
+        x, xs, block = X.codes, X.scales, X.block
+        M, K = x.shape
+        _is(x, (M, K), torch.uint8)
+        _is(xs, (M, K // block if block > 0 else 1), torch.float32)
+    else:
+        x, xs, block = X, None, 0
+        M, K = x.shape
+        _is(x, (M, K), torch.bfloat16)
+    if K != w.n_in:
+        raise ValueError(f"X has {K} columns, the weight {w.n_in} rows")
+    bf16 = torch.bfloat16
+    r = 0 if A is None else A.shape[1]
+    _is(A, (K, r), bf16)
+    _is(B, (r, w.n_out), bf16)
+    if Y is None:
+        Y = _empty((M, w.n_out), bf16, x.device, stream)
+    _is(Y, (M, w.n_out), bf16)
+    if not save_V or r == 0:
+        V = None
+    elif V is None:
+        V = _empty((M, r), bf16, x.device, stream)
+    _is(V, (M, r), bf16)
+    buf = workspace.get(max(_WS_PREFIX, qlora_workspace_bytes(QLORA_OP_MATVEC, M, K, w.n_out, r)), stream)
+    ws = w.c_struct()
+    _check(lib().qlora_matvec(ctypes.byref(ws), _ptr(x), _ptr(xs), block, M, _ptr(A), _ptr(B), r, adapter_scale,
+                              _ptr(Y), _ptr(V), _ptr(buf), buf.numel(), _stream(stream)), "qlora_matvec")
+    return Y, V
 
 
 # ---------------------------------------------------------------- compositions

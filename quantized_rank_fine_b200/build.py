@@ -22,8 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqlora.so")
 SOURCES = ["api.cu", "quantize.cu", "dequant.cu", "skinny.cu", "gemm.cu", "gemv.cu", "xa_small.cu", "noalloc.cu",
-           "intq.cu", "selftest.cu"]
-HEADERS = ["common.cuh", "kernels.h", "sm100.cuh"]
+           "intq.cu", "selftest.cu", "dropout.cu", "rmsnorm.cu", "matvec.cu"]
+HEADERS = ["common.cuh", "kernels.h", "sm100.cuh", "philox.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--ptxas-options=--warn-on-spills"]

@@ -20,8 +20,6 @@ namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // Current device must be compute capability 10.0 (B200 / sm_100).
 qlora_status check_device() {
   static int checked[64] = {};   // 0 unknown, 1 ok, 2 unsupported
@@ -38,8 +36,8 @@ qlora_status check_device() {
   return checked[dev] == 1 ? QLORA_OK : QLORA_ERR_UNSUPPORTED_DEVICE;
 }
 
-// A required tensor: non-NULL, device (or managed) memory of the current device, 16-byte aligned.
-qlora_status check_ptr(const void* p, bool required = true) {
+// A required tensor: non-NULL, device (or managed) memory of the current device, aligned (16 bytes).
+qlora_status check_ptr(const void* p, bool required = true, uintptr_t align = 16) {
   if (!p) return required ? QLORA_ERR_INVALID_ARG : QLORA_OK;
   cudaPointerAttributes a;
   if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
@@ -50,7 +48,7 @@ qlora_status check_ptr(const void* p, bool required = true) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (a.device != dev) return QLORA_ERR_INVALID_ARG;
-  if (!aligned16(p)) return QLORA_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(p) & (align - 1)) != 0) return QLORA_ERR_ALIGNMENT;
   return QLORA_OK;
 }
 
@@ -70,6 +68,31 @@ bool rank_ok(int r) { return r >= 8 && r <= 256 && r % 8 == 0; }
 bool linear_shape_ok(int64_t M, int64_t in, int64_t out, int r) {
   return M >= 1 && M <= (int64_t(1) << 31) - 1 && in >= 64 && out >= 64 && in % 64 == 0 && out % 64 == 0 &&
          in <= (int64_t(1) << 24) && out <= (int64_t(1) << 24) && rank_ok(r);
+}
+
+bool matvec_shape_ok(int64_t M, int64_t in, int64_t out, int r) {
+  return M <= qlora::kGemvMaxTokens && linear_shape_ok(M, in, out, r == 0 ? 8 : r);
+}
+
+bool norm_shape_ok(int64_t M, int64_t n) {
+  return M >= 1 && M <= (int64_t(1) << 31) - 1 && n >= 8 && n % 8 == 0 && n <= qlora::kNormMaxCols;
+}
+
+// The generator's numbers for the kernels; `on` stays 0 for p = 0 (nothing is
+// dropped or scaled).  The device counter is looked at with the other pointers.
+qlora_status read_dropout(const qlora_dropout* d, qlora::DropoutCounter& c, float& keep_scale) {
+  c = qlora::DropoutCounter{};
+  keep_scale = 1.0f;
+  if (!d) return QLORA_OK;
+  if (!(d->p >= 0.0f && d->p < 1.0f)) return QLORA_ERR_INVALID_ARG;
+  if (d->p == 0.0f) return QLORA_OK;
+  c.on = 1;
+  c.threshold = static_cast<uint32_t>(std::rint(static_cast<double>(d->p) * 4294967296.0));
+  c.seed = d->seed;
+  c.offset = d->offset;
+  c.counter = d->counter;
+  keep_scale = static_cast<float>(1.0 / (1.0 - static_cast<double>(d->p)));
+  return QLORA_OK;
 }
 
 qlora_status check_weight_shape(const qlora_nf4_weight* w) {
@@ -125,6 +148,8 @@ WsLayout ws_layout(int op, int64_t M, int64_t in, int64_t out, int r) {
   L.total = off + align256(part);
   return L;
 }
+
+size_t matvec_ws_bytes(int64_t M, int r) { return kFixedBytes + align256(static_cast<size_t>(M) * r * 2); }
 
 struct SplitRegion {
   uint32_t* counters;
@@ -183,7 +208,7 @@ void timing_after(int which, cudaStream_t stream) {
 extern "C" {
 
 qlora_status qlora_time_kernel(int which, void* const* starts, void* const* stops, int n) {
-  if (n < 0 || which < QLORA_KERNEL_QUANTIZE || which > QLORA_KERNEL_GEMV) return QLORA_ERR_INVALID_ARG;
+  if (n < 0 || which < QLORA_KERNEL_QUANTIZE || which > QLORA_KERNEL_RMSNORM_BWD) return QLORA_ERR_INVALID_ARG;
   if (n > 0 && (!starts || !stops)) return QLORA_ERR_INVALID_ARG;
   g_hook.which = n > 0 ? which : 0;
   g_hook.starts = starts;
@@ -217,6 +242,7 @@ void qlora_nf4_codebook(float out[16]) {
 int64_t qlora_adapter_params(int64_t in, int64_t out, int r) { return static_cast<int64_t>(r) * (in + out); }
 
 size_t qlora_workspace_bytes(int op, int64_t M, int64_t in, int64_t out, int r) {
+  if (op == QLORA_OP_MATVEC) return matvec_shape_ok(M, in, out, r) ? matvec_ws_bytes(M, r) : 0;
   if ((op != QLORA_OP_FWD && op != QLORA_OP_BWD) || !linear_shape_ok(M, in, out, r)) return 0;
   return ws_layout(op, M, in, out, r).total;
 }
@@ -415,10 +441,17 @@ struct LinearOpts {
 static qlora_status read_opts(const qlora_linear_opts* o, LinearOpts& lo) {
   lo = LinearOpts{};
   if (!o) return QLORA_OK;
-  if (!std::isfinite(o->adapter_scale) || (o->flags & ~static_cast<uint32_t>(QLORA_ACCUMULATE_GRADS)) != 0u)
+  if (!std::isfinite(o->adapter_scale) ||
+      (o->flags & ~static_cast<uint32_t>(QLORA_ACCUMULATE_GRADS | QLORA_DROPOUT_COUNTER)) != 0u)
     return QLORA_ERR_INVALID_ARG;
   lo.scale = o->adapter_scale;
   lo.accumulate = (o->flags & QLORA_ACCUMULATE_GRADS) != 0u;
+  if (o->flags & QLORA_DROPOUT_COUNTER) {
+    if (o->dropout_keep) return QLORA_ERR_INVALID_ARG;
+    QLORA_TRY(read_dropout(&o->dropout, lo.drop.ctr, lo.drop.keep_scale));
+    if (lo.drop.ctr.on) QLORA_TRY(check_ptr(lo.drop.ctr.counter, false, 8));
+    return QLORA_OK;
+  }
   if (o->dropout_keep) {
     if (!(o->dropout_p >= 0.0f && o->dropout_p < 1.0f)) return QLORA_ERR_INVALID_ARG;
     QLORA_TRY(check_ptr(o->dropout_keep));
@@ -598,6 +631,117 @@ qlora_status qlora_linear_bwd_adam(const qlora_nf4_weight* w, const uint16_t* X,
     QLORA_CUDA(qlora::launch_dx_gemm(wv, dY, U, A, M, r, dX, status, sr.counters, sr.partials, sr.partial_bytes, s));
   }
   QLORA_CUDA(qlora::launch_dbda(V, dY, X, U, M, w->in, w->out, r, nullptr, nullptr, status, s, &pA, &pB));
+  return QLORA_OK;
+}
+
+qlora_status qlora_dropout_mask(const qlora_dropout* d, int64_t M, int64_t n, uint8_t* keep, void* stream) {
+  if (!d || !keep) return QLORA_ERR_INVALID_ARG;
+  qlora::DropoutCounter c;
+  float keep_scale;
+  QLORA_TRY(read_dropout(d, c, keep_scale));
+  if (M < 1 || n < 1 || M > (int64_t(1) << 40) / n) return QLORA_ERR_SHAPE;
+  QLORA_TRY(check_device());
+  QLORA_TRY(check_ptr(keep));
+  QLORA_TRY(check_ptr(c.counter, false, 8));
+  QLORA_CUDA(qlora::launch_dropout_mask(c, M * n, keep, static_cast<cudaStream_t>(stream)));
+  return QLORA_OK;
+}
+
+qlora_status qlora_rmsnorm_fwd(const uint16_t* X, const uint16_t* R, const void* G, int g_dtype, float eps, int64_t M,
+                               int64_t n, const qlora_dropout* drop, uint16_t* H, uint16_t* Y, uint8_t* Q,
+                               float* q_scales, int q_block, float* rstd, void* stream) {
+  if (!X || !G || (!Y && !Q) || (Q && !q_scales) || (g_dtype != QLORA_F32 && g_dtype != QLORA_BF16) ||
+      !(eps > 0.0f) || !std::isfinite(eps) || (Q && q_block != 0 && q_block != 64))
+    return QLORA_ERR_INVALID_ARG;
+  qlora::NormFwd a{};
+  QLORA_TRY(read_dropout(drop, a.drop, a.keep_scale));
+  if (!norm_shape_ok(M, n) || (Q && q_block == 64 && n % 64 != 0)) return QLORA_ERR_SHAPE;
+  QLORA_TRY(check_device());
+  for (const void* p : {static_cast<const void*>(X), G}) QLORA_TRY(check_ptr(p));
+  for (const void* p : {static_cast<const void*>(R), static_cast<const void*>(H), static_cast<const void*>(Y),
+                        static_cast<const void*>(Q), static_cast<const void*>(rstd)})
+    QLORA_TRY(check_ptr(p, false));
+  if (Q) QLORA_TRY(check_ptr(q_scales));
+  QLORA_TRY(check_ptr(a.drop.counter, false, 8));
+  a.X = X;
+  a.R = R;
+  a.G = G;
+  a.g_f32 = g_dtype == QLORA_F32;
+  a.eps = eps;
+  a.M = M;
+  a.n = n;
+  a.H = H;
+  a.Y = Y;
+  a.Q = Q;
+  a.q_scales = q_scales;
+  a.q_block = q_block;
+  a.rstd = rstd;
+  QLORA_CUDA(qlora::launch_rmsnorm_fwd(a, static_cast<cudaStream_t>(stream)));
+  return QLORA_OK;
+}
+
+size_t qlora_rmsnorm_ws_bytes(int64_t M, int64_t n) {
+  return norm_shape_ok(M, n) ? kFixedBytes + align256(qlora::norm_bwd_parts_bytes(M, n)) : 0;
+}
+
+qlora_status qlora_rmsnorm_bwd(const uint16_t* dY, const uint16_t* H, const void* G, int g_dtype, const float* rstd,
+                               const uint16_t* dH, int64_t M, int64_t n, const qlora_dropout* drop, uint16_t* dR,
+                               uint16_t* dX, float* dG, uint32_t flags, void* ws, size_t ws_bytes, void* stream) {
+  if (!dY || !H || !G || !rstd || !dR || (g_dtype != QLORA_F32 && g_dtype != QLORA_BF16) ||
+      (flags & ~static_cast<uint32_t>(QLORA_ACCUMULATE_GRADS)) != 0u)
+    return QLORA_ERR_INVALID_ARG;
+  qlora::NormBwd a{};
+  QLORA_TRY(read_dropout(drop, a.drop, a.keep_scale));
+  if (dX && !a.drop.on) return QLORA_ERR_INVALID_ARG;
+  if (!norm_shape_ok(M, n)) return QLORA_ERR_SHAPE;
+  if (dG && (!ws || ws_bytes < qlora_rmsnorm_ws_bytes(M, n))) return QLORA_ERR_WORKSPACE;
+  QLORA_TRY(check_device());
+  for (const void* p : {static_cast<const void*>(dY), static_cast<const void*>(H), G, static_cast<const void*>(rstd),
+                        static_cast<const void*>(dR)})
+    QLORA_TRY(check_ptr(p));
+  for (const void* p : {static_cast<const void*>(dH), static_cast<const void*>(dX), static_cast<const void*>(dG)})
+    QLORA_TRY(check_ptr(p, false));
+  if (dG) QLORA_TRY(check_ptr(ws));
+  QLORA_TRY(check_ptr(a.drop.counter, false, 8));
+  a.dY = dY;
+  a.H = H;
+  a.G = G;
+  a.g_f32 = g_dtype == QLORA_F32;
+  a.rstd = rstd;
+  a.dH = dH;
+  a.M = M;
+  a.n = n;
+  a.dR = dR;
+  a.dX = dX;
+  a.dG = dG;
+  a.accumulate = (flags & QLORA_ACCUMULATE_GRADS) != 0u;
+  a.parts = dG ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kFixedBytes) : nullptr;
+  QLORA_CUDA(qlora::launch_rmsnorm_bwd(a, static_cast<cudaStream_t>(stream)));
+  return QLORA_OK;
+}
+
+qlora_status qlora_matvec(const qlora_nf4_weight* w, const void* X, const float* x_scales, int x_block, int64_t M,
+                          const uint16_t* A, const uint16_t* B, int r, float adapter_scale, uint16_t* Y,
+                          uint16_t* V_save, void* ws, size_t ws_bytes, void* stream) {
+  if (!X || !Y || (r != 0) != (A != nullptr) || (r != 0) != (B != nullptr) || (r == 0 && V_save) ||
+      (x_scales && x_block != 0 && x_block != 64) || !std::isfinite(adapter_scale))
+    return QLORA_ERR_INVALID_ARG;
+  QLORA_TRY(check_weight_shape(w));
+  if (w->dq_format != QLORA_FMT_INT16) return QLORA_ERR_INVALID_ARG;
+  if (!matvec_shape_ok(M, w->in, w->out, r)) return QLORA_ERR_SHAPE;
+  if (!ws || ws_bytes < matvec_ws_bytes(M, r)) return QLORA_ERR_WORKSPACE;
+  QLORA_TRY(check_device());
+  QLORA_TRY(check_weight(w));
+  for (const void* p : {X, static_cast<const void*>(Y), static_cast<const void*>(ws)}) QLORA_TRY(check_ptr(p));
+  for (const void* p : {static_cast<const void*>(x_scales), static_cast<const void*>(A), static_cast<const void*>(B),
+                        static_cast<const void*>(V_save)})
+    QLORA_TRY(check_ptr(p, false));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  uint16_t* V = V_save ? V_save : reinterpret_cast<uint16_t*>(base + kFixedBytes);
+  const qlora::ActView x{X, x_scales, x_block};
+  if (r) QLORA_CUDA(qlora::launch_xa_small_act(x, A, M, w->in, r, V, s, adapter_scale));
+  QLORA_CUDA(qlora::launch_matvec(view(w), x, V, B, M, r, Y, reinterpret_cast<uint32_t*>(base), s));
   return QLORA_OK;
 }
 

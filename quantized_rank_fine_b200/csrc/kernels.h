@@ -93,10 +93,23 @@ struct AdamParams {
 // Dropout on the low-rank intermediate: with keep != nullptr (device, M x r,
 // 1 = keep) every stored element of V and U is also multiplied by keep_scale
 // (1 / (1 - p)) where it is kept and by 0 where it is dropped.
+//
+// With on != 0 the mask comes from the counter instead (philox.cuh): element
+// row r + col is kept where its 32-bit word is at least `threshold`.
+struct DropoutCounter {
+  int on = 0;
+  uint32_t threshold = 0;
+  uint64_t seed = 0;
+  uint64_t offset = 0;
+  const uint64_t* counter = nullptr;   // device, added to offset; may be nullptr
+};
 struct Dropout {
   const uint8_t* keep = nullptr;
   float keep_scale = 1.0f;
+  DropoutCounter ctr;
 };
+// The counter's mask of n elements as bytes (1 = keep); keep 16-byte aligned.
+cudaError_t launch_dropout_mask(const DropoutCounter& d, int64_t n, uint8_t* keep, cudaStream_t stream);
 cudaError_t launch_xa(const uint16_t* X, const uint16_t* A, int64_t M, int64_t n_in, int r, uint16_t* V,
                       uint32_t* status, cudaStream_t stream, float scale = 1.0f, Dropout drop = {});
 cudaError_t launch_dybt(const uint16_t* dY, const uint16_t* B, int64_t M, int64_t n_out, int r,
@@ -120,6 +133,60 @@ cudaError_t launch_xa_small(const uint16_t* X, const uint16_t* A, int64_t M, int
                             cudaStream_t stream, float scale = 1.0f, Dropout drop = {});
 cudaError_t launch_gemv(const WeightView& w, const uint16_t* X, const uint16_t* V, const uint16_t* B, int64_t M,
                         int r, uint16_t* Y, uint32_t* status, cudaStream_t stream);
+
+// X of the matrix-vector product: bf16 (scales == nullptr), or E4M3 codes with one
+// fp32 scale per row (block 0) or per 64 columns (block 64).
+struct ActView {
+  const void* x;
+  const float* scales;
+  int block;
+};
+// V = X A as launch_xa_small, for X in 8 bits too.
+cudaError_t launch_xa_small_act(const ActView& x, const uint16_t* A, int64_t M, int64_t K, int r, uint16_t* V,
+                                cudaStream_t stream, float scale);
+// Y = X w' + V B for an integer weight (kFmtInt16), M <= kGemvMaxTokens; r = 0
+// leaves the adapter term out.
+cudaError_t launch_matvec(const WeightView& w, const ActView& x, const uint16_t* V, const uint16_t* B, int64_t M,
+                          int r, uint16_t* Y, uint32_t* status, cudaStream_t stream);
+
+// Residual addition and RMS norm (see qlora_rmsnorm_fwd); null pointers leave a
+// part out.  n is a multiple of 8, at most kNormMaxCols.
+constexpr int64_t kNormMaxCols = 65536;
+struct NormFwd {
+  const uint16_t* X;
+  const uint16_t* R;
+  const void* G;
+  bool g_f32;
+  float eps;
+  int64_t M, n;
+  DropoutCounter drop;
+  float keep_scale;
+  uint16_t* H;
+  uint16_t* Y;
+  uint8_t* Q;
+  float* q_scales;
+  int q_block;
+  float* rstd;
+};
+cudaError_t launch_rmsnorm_fwd(const NormFwd& a, cudaStream_t stream);
+struct NormBwd {
+  const uint16_t* dY;
+  const uint16_t* H;
+  const void* G;
+  bool g_f32;
+  const float* rstd;
+  const uint16_t* dH;
+  int64_t M, n;
+  DropoutCounter drop;
+  float keep_scale;
+  uint16_t* dR;
+  uint16_t* dX;
+  float* dG;
+  bool accumulate;
+  float* parts;     // scratch of norm_bwd_parts_bytes(M, n) when dG is asked for
+};
+size_t norm_bwd_parts_bytes(int64_t M, int64_t n);
+cudaError_t launch_rmsnorm_bwd(const NormBwd& a, cudaStream_t stream);
 
 // Fused dequant GEMMs (tcgen05, persistent grid); `status` is the workspace
 // status word.  When the tile count does not divide evenly over the CTAs the

@@ -21,6 +21,7 @@
 // follow those of the first in the grid, and both use the same split count.
 #include "common.cuh"
 #include "kernels.h"
+#include "philox.cuh"
 #include "sm100.cuh"
 
 #include <cudaTypedefs.h>
@@ -57,6 +58,7 @@ struct SkArgs {
   int accumulate;        // out_kind 1 or 2: add to the stored values instead of overwriting
   const uint8_t* keep;   // out_kind 0: dropout keep mask [row][r] (1 = keep), or nullptr
   float keep_scale;      // factor of the kept values (1 / (1 - p))
+  DropoutCounter ctr;    // out_kind 0: the mask from the counter instead, if ctr.on
 };
 
 // One Adam / AdamW step of parameter element i with gradient g (fp32, IEEE
@@ -92,6 +94,12 @@ __device__ __forceinline__ void store_pair(const SkArgs& p, int64_t row, int col
       const uint8_t* k = p.keep + row * p.r + col;
       v0 *= k[0] ? p.keep_scale : 0.0f;
       v1 *= k[1] ? p.keep_scale : 0.0f;
+    } else if (p.ctr.on) {
+      // r and col are even, so the pair is words 0, 1 or 2, 3 of one Philox block
+      const int64_t e = row * p.r + col;
+      const uint4 u = philox4x32_10(static_cast<uint64_t>(e >> 2), dropout_offset(p.ctr), p.ctr.seed);
+      v0 *= ((e & 2) ? u.z : u.x) >= p.ctr.threshold ? p.keep_scale : 0.0f;
+      v1 *= ((e & 2) ? u.w : u.y) >= p.ctr.threshold ? p.keep_scale : 0.0f;
     }
     *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + row * p.r + col) = pack_bf16x2(v0, v1);
   } else if (p.out_kind == 1) {
@@ -378,7 +386,7 @@ cudaError_t run(const Product& x, const Product* y, int r, int64_t k_total, uint
   const Plan pl = plan(x.rows, r, k_total, y ? y->rows : 0, resident);
   auto args = [&](const Product& q) {
     return SkArgs{q.rows, r, k_total, pl.kps, q.out, q.out_kind, status, q.adam ? 1 : 0,
-                  q.adam ? *q.adam : AdamParams{}, q.scale, accumulate ? 1 : 0, q.drop.keep, q.drop.keep_scale};
+                  q.adam ? *q.adam : AdamParams{}, q.scale, accumulate ? 1 : 0, q.drop.keep, q.drop.keep_scale, q.drop.ctr};
   };
   const SkArgs a0 = args(x), a1 = y ? args(*y) : a0;
   const int rt0 = static_cast<int>((x.rows + kRowsT - 1) / kRowsT);
