@@ -69,7 +69,7 @@ typedef enum qlora_status {
 typedef enum qlora_dtype { QLORA_F32 = 0, QLORA_BF16 = 1 } qlora_dtype;
 
 /* Operation whose workspace size qlora_workspace_bytes() reports. */
-typedef enum qlora_op { QLORA_OP_FWD = 1, QLORA_OP_BWD = 2, QLORA_OP_MATVEC = 3 } qlora_op;
+typedef enum qlora_op { QLORA_OP_FWD = 1, QLORA_OP_BWD = 2 } qlora_op;
 
 /* Fixed format constants. */
 #define QLORA_BLOCK 64   /* weights per absmax block */
@@ -509,9 +509,11 @@ QLORA_API size_t qlora_rmsnorm_ws_bytes(int64_t M, int64_t n);
  * A few tokens through an integer weight (dq_format QLORA_FMT_INT16: 4-bit codes,
  * one scale per 16 weights), with or without adapters -- the decode step of a
  * layer on that base, at the speed of reading the weight once:
- *   V = bf16(s X A),   Y = bf16(X w' + V B),   w' = (code - 8) scale
- * with fp32 accumulation; unlike qlora_linear_fwd it does not round w' to bf16 and
- * it reads 8-bit activations as qlora_rmsnorm_fwd writes them.
+ *   Y = bf16(X w' + s (X A) B),   V = bf16(s X A),   w' = (code - 8) scale
+ * with fp32 accumulation.  Unlike qlora_linear_fwd it does not round w' or the V in
+ * Y to bf16 (it rounds the products x scale instead, once, to bf16), and it reads
+ * 8-bit activations as qlora_rmsnorm_fwd writes them.  It needs no workspace, and
+ * calls on different streams do not touch each other.
  *   w         [host] descriptor; another format is QLORA_ERR_INVALID_ARG.
  *   X         [device] bf16 (M, in), or with x_scales uint8 (M, in) E4M3 codes.
  *   x_scales  [device] fp32 (M, in / 64) for x_block = 64, (M) for x_block = 0:
@@ -520,19 +522,16 @@ QLORA_API size_t qlora_rmsnorm_ws_bytes(int64_t M, int64_t n);
  *   r         0, or 8 <= r <= 256 with r % 8 == 0.
  *   s         adapter_scale, finite.
  *   Y         [device] out: bf16 (M, out).
- *   V_save    [device] out: bf16 (M, r), or NULL (V then lives in the workspace).
- *   ws        [device] at least qlora_workspace_bytes(QLORA_OP_MATVEC, ...) bytes,
- *             initialised by qlora_ws_init (it may be the layer's).
+ *   V_save    [device] out: V, bf16 (M, r), or NULL.
  * QLORA_ERR_SHAPE unless 1 <= M <= 16, in % 64 == 0 and out % 64 == 0.
  */
 QLORA_API qlora_status qlora_matvec(const qlora_nf4_weight* w, const void* X, const float* x_scales, int x_block,
                                     int64_t M, const uint16_t* A, const uint16_t* B, int r, float adapter_scale,
-                                    uint16_t* Y, uint16_t* V_save, void* ws, size_t ws_bytes, void* stream);
+                                    uint16_t* Y, uint16_t* V_save, void* stream);
 
 /* ---------------------------------------------------------------- helpers */
 
-/* Bytes of workspace qlora_linear_fwd / qlora_linear_bwd / qlora_matvec
- * (QLORA_OP_MATVEC: the prefix and V, r = 0 allowed) use at these sizes on
+/* Bytes of workspace qlora_linear_fwd / qlora_linear_bwd use at these sizes on
  * the current device (0 for an unknown op or invalid sizes).  Host only: it reads
  * the device's SM count, no device memory.
  * Layout: a 1280-byte prefix (the 256-byte status word, then 1 KB of counters

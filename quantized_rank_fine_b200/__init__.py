@@ -22,7 +22,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqlora.so")
 
 QLORA_F32, QLORA_BF16 = 0, 1
-QLORA_OP_FWD, QLORA_OP_BWD, QLORA_OP_MATVEC = 1, 2, 3
+QLORA_OP_FWD, QLORA_OP_BWD = 1, 2
 BLOCK, GROUP = 64, 256
 _WS_PREFIX = 1280   # bytes of a workspace that every call needs
 
@@ -135,7 +135,7 @@ def lib() -> ctypes.CDLL:
             "qlora_rmsnorm_fwd": (i32, [vp, vp, vp, i32, f32, i64, i64, dp, vp, vp, vp, vp, i32, vp, vp]),
             "qlora_rmsnorm_bwd": (i32, [vp, vp, vp, i32, vp, vp, i64, i64, dp, vp, vp, vp, u32, vp, sz, vp]),
             "qlora_rmsnorm_ws_bytes": (sz, [i64, i64]),
-            "qlora_matvec": (i32, [wp, vp, vp, i32, i64, vp, vp, i32, f32, vp, vp, vp, sz, vp]),
+            "qlora_matvec": (i32, [wp, vp, vp, i32, i64, vp, vp, i32, f32, vp, vp, vp]),
             "qlora_linear_fwd_ex": (i32, [wp, vp, i64, vp, vp, i32, vp, vp, ctypes.POINTER(_LinearOpts), vp, sz,
                                           vp]),
             "qlora_linear_bwd_ex": (i32, [wp, vp, vp, vp, i64, vp, vp, i32, vp, vp, vp,
@@ -171,14 +171,34 @@ def _empty(shape, dtype, device, stream=None):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _is(t, shape, *dtypes):
-    """Refuse a tensor of another shape or type: the C calls see pointers only."""
-    if t is not None and (t.dtype not in dtypes or t.shape != shape):
-        raise ValueError(f"expected {tuple(shape)} of {' or '.join(map(str, dtypes))}, got {tuple(t.shape)} of {t.dtype}")
+def _empty_like(t, dtype, stream=None):
+    """_empty with the shape and device of t (the shorter way through torch)."""
+    if stream is None or not isinstance(stream, torch.cuda.Stream):
+        return torch.empty_like(t, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, dtype=dtype)
+
+
+def _arg(t, shape, dtype):
+    """The pointer of an optional tensor, refused where its shape, type or layout is
+    another: the C calls see pointers only."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"expected {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+# torch's current stream as a raw handle, without the Python object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream=None):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
@@ -549,9 +569,15 @@ class RMSNormOut:
     rstd: torch.Tensor | None   # float32 (M)
 
 
-def _gain_dtype(G, n):
-    _is(G, (n,), torch.float32, torch.bfloat16)
-    return QLORA_F32 if G.dtype == torch.float32 else QLORA_BF16
+_GAIN_DTYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
+
+
+def _gain(G, n):
+    """Pointer and type code of a gain of n values."""
+    code = _GAIN_DTYPES.get(G.dtype)
+    if code is None:
+        raise ValueError("the gain must be fp32 or bf16")
+    return _arg(G, (n,), G.dtype), code
 
 
 def qlora_rmsnorm_fwd(X: torch.Tensor, G: torch.Tensor, eps: float = 1e-5, residual=None,
@@ -561,25 +587,26 @@ def qlora_rmsnorm_fwd(X: torch.Tensor, G: torch.Tensor, eps: float = 1e-5, resid
     bf16 or fp32.  The result holds H (only with a residual or dropout: else h is X
     itself), Y = bf16(y) unless want_y is False, y in 8 bits with quant_block 0 (one
     scale a row) or 64 (one per 64 columns), and rstd for the backward."""
-    M, n = X.shape
-    bf16 = torch.bfloat16
-    for t in (X, residual, H, Y):
-        _is(t, (M, n), bf16)
-    d = _drop(dropout)
-    gd = _gain_dtype(G, n)
-    dev = X.device
-    if H is None and (residual is not None or d is not None):
-        H = _empty((M, n), bf16, dev, stream)
+    shape, bf16 = X.shape, torch.bfloat16
+    M, n = shape
+    x, res = _arg(X, shape, bf16), _arg(residual, shape, bf16)
+    gain, gain_code = _gain(G, n)
+    drop = _drop(dropout)
+    if H is None and (residual is not None or drop is not None):
+        H = _empty_like(X, bf16, stream)
     if Y is None and want_y:
-        Y = _empty((M, n), bf16, dev, stream)
-    act = None
+        Y = _empty_like(X, bf16, stream)
+    act = codes = scales = rstd = None
     if quant_block is not None:
-        nb = n // quant_block if quant_block > 0 else 1
-        act = Act8(_empty((M, n), torch.uint8, dev, stream), _empty((M, nb), torch.float32, dev, stream), quant_block)
-    rstd = _empty((M,), torch.float32, dev, stream) if save_rstd else None
-    _check(lib().qlora_rmsnorm_fwd(_ptr(X), _ptr(residual), _ptr(G), gd, eps, M, n, d, _ptr(H), _ptr(Y),
-                                   _ptr(act.codes) if act else None, _ptr(act.scales) if act else None,
-                                   quant_block or 0, _ptr(rstd), _stream(stream)), "qlora_rmsnorm_fwd")
+        act = Act8(_empty_like(X, torch.uint8, stream),
+                   _empty((M, n // quant_block if quant_block > 0 else 1), torch.float32, X.device, stream),
+                   quant_block)
+        codes, scales = act.codes.data_ptr(), act.scales.data_ptr()
+    if save_rstd:
+        rstd = _empty((M,), torch.float32, X.device, stream)
+    _check(lib().qlora_rmsnorm_fwd(x, res, gain, gain_code, eps, M, n, drop, _arg(H, shape, bf16),
+                                   _arg(Y, shape, bf16), codes, scales, quant_block or 0,
+                                   rstd.data_ptr() if save_rstd else None, _stream(stream)), "qlora_rmsnorm_fwd")
     return RMSNormOut(H, Y, act, rstd)
 
 
@@ -592,63 +619,63 @@ def qlora_rmsnorm_bwd(dY: torch.Tensor, H: torch.Tensor, G: torch.Tensor, rstd: 
     Without dropout dX is dR.  With accumulate dG (given) receives the sum."""
     if accumulate and dG is None:
         raise ValueError("accumulate needs the dG to add into")
-    M, n = H.shape
-    bf16 = torch.bfloat16
-    for t in (dY, H, dH, dR, dX):
-        _is(t, (M, n), bf16)
-    _is(rstd, (M,), torch.float32)
-    _is(dG, (n,), torch.float32)
-    d = _drop(dropout)
-    gd = _gain_dtype(G, n)
+    shape, bf16, f32 = H.shape, torch.bfloat16, torch.float32
+    M, n = shape
+    h, dy, dh = _arg(H, shape, bf16), _arg(dY, shape, bf16), _arg(dH, shape, bf16)
+    gain, gain_code = _gain(G, n)
+    rs = _arg(rstd, (M,), f32)
+    drop = _drop(dropout)
+    dg = ws = None
+    nb = 0
+    if need_dG:
+        dg = _arg(dG, (n,), f32)
+        if dG is None:
+            dG = _empty((n,), f32, H.device, stream)
+            dg = dG.data_ptr()
+        buf = workspace.get(max(_WS_PREFIX, lib().qlora_rmsnorm_ws_bytes(M, n)), stream)
+        ws, nb = buf.data_ptr(), buf.numel()
     if dR is None:
-        dR = _empty((M, n), bf16, H.device, stream)
-    if d is None:
+        dR = _empty_like(H, bf16, stream)
+    if drop is None:
         dX = None
     elif dX is None:
-        dX = _empty((M, n), bf16, H.device, stream)
-    buf = None
-    if need_dG:
-        if dG is None:
-            dG = _empty((n,), torch.float32, H.device, stream)
-        buf = workspace.get(max(_WS_PREFIX, lib().qlora_rmsnorm_ws_bytes(M, n)), stream)
-    _check(lib().qlora_rmsnorm_bwd(_ptr(dY), _ptr(H), _ptr(G), gd, _ptr(rstd), _ptr(dH), M, n, d, _ptr(dR), _ptr(dX),
-                                   _ptr(dG) if need_dG else None, QLORA_ACCUMULATE_GRADS if accumulate else 0,
-                                   _ptr(buf), buf.numel() if need_dG else 0, _stream(stream)), "qlora_rmsnorm_bwd")
-    return (dR if d is None else dX), dR, (dG if need_dG else None)
+        dX = _empty_like(H, bf16, stream)
+    _check(lib().qlora_rmsnorm_bwd(dy, h, gain, gain_code, rs, dh, M, n, drop, _arg(dR, shape, bf16),
+                                   _arg(dX, shape, bf16), dg, QLORA_ACCUMULATE_GRADS if accumulate else 0, ws, nb,
+                                   _stream(stream)), "qlora_rmsnorm_bwd")
+    return (dR if drop is None else dX), dR, (dG if need_dG else None)
 
 
-def qlora_matvec(w: NF4Weight, X, workspace: Workspace, A=None, B=None, adapter_scale: float = 1.0,
+def qlora_matvec(w: NF4Weight, X, workspace: Workspace | None = None, A=None, B=None, adapter_scale: float = 1.0,
                  save_V: bool = False, stream=None, Y=None, V=None):
     """Up to 16 tokens through an integer weight (int_weight): X is bf16 (M, in) or
     the Act8 that qlora_rmsnorm_fwd returns; A and B the adapters, or None.  Returns
-    (Y, V), V = s X A with save_V and adapters, else None."""
+    (Y, V), V = s X A with save_V and adapters, else None.  The call needs no scratch:
+    `workspace` is accepted, as in the layer's calls, and left alone."""
+    bf16 = torch.bfloat16
+    scales, block = None, 0
     if isinstance(X, Act8):
-        x, xs, block = X.codes, X.scales, X.block
-        M, K = x.shape
-        _is(x, (M, K), torch.uint8)
-        _is(xs, (M, K // block if block > 0 else 1), torch.float32)
+        act, X, block = X, X.codes, X.block
+        M, K = X.shape
+        x = _arg(X, (M, K), torch.uint8)
+        scales = _arg(act.scales, (M, K // block if block > 0 else 1), torch.float32)
     else:
-        x, xs, block = X, None, 0
-        M, K = x.shape
-        _is(x, (M, K), torch.bfloat16)
+        M, K = X.shape
+        x = _arg(X, (M, K), bf16)
+    N = w.n_out
     if K != w.n_in:
         raise ValueError(f"X has {K} columns, the weight {w.n_in} rows")
-    bf16 = torch.bfloat16
     r = 0 if A is None else A.shape[1]
-    _is(A, (K, r), bf16)
-    _is(B, (r, w.n_out), bf16)
     if Y is None:
-        Y = _empty((M, w.n_out), bf16, x.device, stream)
-    _is(Y, (M, w.n_out), bf16)
+        Y = _empty((M, N), bf16, X.device, stream)
     if not save_V or r == 0:
         V = None
     elif V is None:
-        V = _empty((M, r), bf16, x.device, stream)
-    _is(V, (M, r), bf16)
-    buf = workspace.get(max(_WS_PREFIX, qlora_workspace_bytes(QLORA_OP_MATVEC, M, K, w.n_out, r)), stream)
+        V = _empty((M, r), bf16, X.device, stream)
     ws = w.c_struct()
-    _check(lib().qlora_matvec(ctypes.byref(ws), _ptr(x), _ptr(xs), block, M, _ptr(A), _ptr(B), r, adapter_scale,
-                              _ptr(Y), _ptr(V), _ptr(buf), buf.numel(), _stream(stream)), "qlora_matvec")
+    _check(lib().qlora_matvec(ctypes.byref(ws), x, scales, block, M, _arg(A, (K, r), bf16), _arg(B, (r, N), bf16), r,
+                              adapter_scale, _arg(Y, (M, N), bf16), _arg(V, (M, r), bf16), _stream(stream)),
+           "qlora_matvec")
     return Y, V
 
 

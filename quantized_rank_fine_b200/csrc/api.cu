@@ -149,8 +149,6 @@ WsLayout ws_layout(int op, int64_t M, int64_t in, int64_t out, int r) {
   return L;
 }
 
-size_t matvec_ws_bytes(int64_t M, int r) { return kFixedBytes + align256(static_cast<size_t>(M) * r * 2); }
-
 struct SplitRegion {
   uint32_t* counters;
   void* partials;
@@ -242,7 +240,6 @@ void qlora_nf4_codebook(float out[16]) {
 int64_t qlora_adapter_params(int64_t in, int64_t out, int r) { return static_cast<int64_t>(r) * (in + out); }
 
 size_t qlora_workspace_bytes(int op, int64_t M, int64_t in, int64_t out, int r) {
-  if (op == QLORA_OP_MATVEC) return matvec_shape_ok(M, in, out, r) ? matvec_ws_bytes(M, r) : 0;
   if ((op != QLORA_OP_FWD && op != QLORA_OP_BWD) || !linear_shape_ok(M, in, out, r)) return 0;
   return ws_layout(op, M, in, out, r).total;
 }
@@ -722,26 +719,21 @@ qlora_status qlora_rmsnorm_bwd(const uint16_t* dY, const uint16_t* H, const void
 
 qlora_status qlora_matvec(const qlora_nf4_weight* w, const void* X, const float* x_scales, int x_block, int64_t M,
                           const uint16_t* A, const uint16_t* B, int r, float adapter_scale, uint16_t* Y,
-                          uint16_t* V_save, void* ws, size_t ws_bytes, void* stream) {
+                          uint16_t* V_save, void* stream) {
   if (!X || !Y || (r != 0) != (A != nullptr) || (r != 0) != (B != nullptr) || (r == 0 && V_save) ||
       (x_scales && x_block != 0 && x_block != 64) || !std::isfinite(adapter_scale))
     return QLORA_ERR_INVALID_ARG;
   QLORA_TRY(check_weight_shape(w));
   if (w->dq_format != QLORA_FMT_INT16) return QLORA_ERR_INVALID_ARG;
   if (!matvec_shape_ok(M, w->in, w->out, r)) return QLORA_ERR_SHAPE;
-  if (!ws || ws_bytes < matvec_ws_bytes(M, r)) return QLORA_ERR_WORKSPACE;
   QLORA_TRY(check_device());
   QLORA_TRY(check_weight(w));
-  for (const void* p : {X, static_cast<const void*>(Y), static_cast<const void*>(ws)}) QLORA_TRY(check_ptr(p));
+  for (const void* p : {X, static_cast<const void*>(Y)}) QLORA_TRY(check_ptr(p));
   for (const void* p : {static_cast<const void*>(x_scales), static_cast<const void*>(A), static_cast<const void*>(B),
                         static_cast<const void*>(V_save)})
     QLORA_TRY(check_ptr(p, false));
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint8_t* base = static_cast<uint8_t*>(ws);
-  uint16_t* V = V_save ? V_save : reinterpret_cast<uint16_t*>(base + kFixedBytes);
-  const qlora::ActView x{X, x_scales, x_block};
-  if (r) QLORA_CUDA(qlora::launch_xa_small_act(x, A, M, w->in, r, V, s, adapter_scale));
-  QLORA_CUDA(qlora::launch_matvec(view(w), x, V, B, M, r, Y, reinterpret_cast<uint32_t*>(base), s));
+  QLORA_CUDA(qlora::launch_matvec(view(w), qlora::ActView{X, x_scales, x_block}, A, B, M, r, adapter_scale, Y, V_save,
+                                  static_cast<cudaStream_t>(stream)));
   return QLORA_OK;
 }
 

@@ -141,13 +141,10 @@ struct ActView {
   const float* scales;
   int block;
 };
-// V = X A as launch_xa_small, for X in 8 bits too.
-cudaError_t launch_xa_small_act(const ActView& x, const uint16_t* A, int64_t M, int64_t K, int r, uint16_t* V,
-                                cudaStream_t stream, float scale);
-// Y = X w' + V B for an integer weight (kFmtInt16), M <= kGemvMaxTokens; r = 0
-// leaves the adapter term out.
-cudaError_t launch_matvec(const WeightView& w, const ActView& x, const uint16_t* V, const uint16_t* B, int64_t M,
-                          int r, uint16_t* Y, uint32_t* status, cudaStream_t stream);
+// Y = X w' + scale (X A) B for an integer weight (kFmtInt16), M <= kGemvMaxTokens;
+// r = 0 leaves the adapter term out; V (M x r) is stored unless nullptr.
+cudaError_t launch_matvec(const WeightView& w, const ActView& x, const uint16_t* A, const uint16_t* B, int64_t M,
+                          int r, float scale, uint16_t* Y, uint16_t* V, cudaStream_t stream);
 
 // Residual addition and RMS norm (see qlora_rmsnorm_fwd); null pointers leave a
 // part out.  n is a multiple of 8, at most kNormMaxCols.

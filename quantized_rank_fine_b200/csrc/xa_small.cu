@@ -25,8 +25,6 @@
 #include "philox.cuh"
 #include "sm100.cuh"
 
-#include <type_traits>
-
 namespace qlora {
 
 namespace {
@@ -52,22 +50,17 @@ struct XaArgs {
   const uint8_t* keep; // dropout keep mask (M, r), 1 = keep, or nullptr
   float keep_scale;    // factor of the kept values (1 / (1 - p))
   DropoutCounter ctr;  // the mask from the counter instead, if ctr.on
-  const float* x_scales;   // kAct8: X holds E4M3 codes with these scales
-  int x_block;             // kAct8: 64 (one scale per 64 columns) or 0 (one per row)
 };
 
-// kAct8: X is 8-bit (code times scale, staged as fp32), else bf16.
-template <bool kAct8>
 __global__ void __launch_bounds__(kXaThreads) xa_small_kernel(const XaArgs p) {
-  using XT = typename std::conditional<kAct8, float, uint16_t>::type;
   // Everything before this kernel has finished once the wait returns, so the
   // dependent launched right after (which reads its own inputs at once) sees
   // them complete.
   grid_dependency_wait();
   grid_launch_dependents();
   extern __shared__ __align__(16) uint8_t smem[];
-  XT* xs = reinterpret_cast<XT*>(smem);                                   // [M][kXPitch]
-  uint16_t* as = reinterpret_cast<uint16_t*>(xs + kGemvMaxTokens * kXPitch);   // [kXaChunk][kXaCols]
+  uint16_t* xs = reinterpret_cast<uint16_t*>(smem);                       // [M][kXPitch]
+  uint16_t* as = xs + kGemvMaxTokens * kXPitch;                           // [kXaChunk][kXaCols]
   float* red = reinterpret_cast<float*>(as + kXaChunk * kXaCols);         // [nkl][P] row lanes
   float* part = red + kXaThreads;                                         // [M x cols]
   float* recv = part + kGemvMaxTokens * kXaCols;                          // [S][cap]
@@ -97,18 +90,8 @@ __global__ void __launch_bounds__(kXaThreads) xa_small_kernel(const XaArgs p) {
     const int xq = n / 8;
     for (int i = tid; i < p.M * xq; i += kXaThreads) {
       const int mm = i / xq, q = i % xq;
-      const int64_t at = static_cast<int64_t>(mm) * p.K + k0 + r0;   // a multiple of 64
-      if constexpr (kAct8) {
-        const uint2 c = reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(p.X) + at)[q];
-        const int64_t k = k0 + r0 + 8 * q;
-        const float s = p.x_scales[p.x_block ? mm * (p.K / 64) + k / 64 : mm];
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          xs[mm * kXPitch + 8 * q + u] =
-              mul_rn(e4m3_to_float(static_cast<uint8_t>((u < 4 ? c.x : c.y) >> (8 * (u & 3)))), s);
-      } else {
-        reinterpret_cast<uint4*>(xs + mm * kXPitch)[q] = reinterpret_cast<const uint4*>(p.X + at)[q];
-      }
+      reinterpret_cast<uint4*>(xs + mm * kXPitch)[q] =
+          reinterpret_cast<const uint4*>(p.X + static_cast<int64_t>(mm) * p.K + k0 + r0)[q];
     }
     // A rows: n x cols bf16 of this column tile
     const int aq = cols / 8;
@@ -123,15 +106,12 @@ __global__ void __launch_bounds__(kXaThreads) xa_small_kernel(const XaArgs p) {
       const int pair = P >= kXaThreads ? tid + kXaThreads * u : tid % P;
       const int j = pair % cw, m = pair / cw;
       if (u < per && j < cols && m < p.M) {
-        const XT* xr = xs + m * kXPitch;
+        const uint16_t* xr = xs + m * kXPitch;
         float s = acc[u];
 #pragma unroll 4
-        for (int k = kl; k < n; k += nkl) {
-          float xv;
-          if constexpr (kAct8) xv = xr[k];
-          else xv = __uint_as_float(static_cast<uint32_t>(xr[k]) << 16);
-          s = fmaf(xv, __uint_as_float(static_cast<uint32_t>(as[k * kXaCols + j]) << 16), s);
-        }
+        for (int k = kl; k < n; k += nkl)
+          s = fmaf(__uint_as_float(static_cast<uint32_t>(xr[k]) << 16),
+                   __uint_as_float(static_cast<uint32_t>(as[k * kXaCols + j]) << 16), s);
         acc[u] = s;
       }
     }
@@ -188,10 +168,8 @@ __global__ void __launch_bounds__(kXaThreads) xa_small_kernel(const XaArgs p) {
   }
 }
 
-constexpr size_t xa_smem_bytes(bool act8) {
-  return kGemvMaxTokens * kXPitch * (act8 ? 4 : 2) + kXaChunk * kXaCols * 2 +
-         (kXaThreads + kGemvMaxTokens * kXaCols + kGemvMaxTokens * kXaCols + kXaMaxCluster) * 4;
-}
+constexpr size_t kXaSmemBytes = (kGemvMaxTokens * kXPitch + kXaChunk * kXaCols) * 2 +
+                                (kXaThreads + kGemvMaxTokens * kXaCols + kGemvMaxTokens * kXaCols + kXaMaxCluster) * 4;
 
 // K-splits (the cluster size): about 256 rows each, at most kXaMaxCluster.
 void xa_plan(int64_t K, int& S, int& Kc) {
@@ -202,27 +180,29 @@ void xa_plan(int64_t K, int& S, int& Kc) {
   Kc = static_cast<int>(kc);
 }
 
-template <bool kAct8>
-cudaError_t run_xa_small(XaArgs a, cudaStream_t stream) {
-  if (a.M < 1 || a.M > kGemvMaxTokens) return cudaErrorInvalidValue;
+}  // namespace
+
+cudaError_t launch_xa_small(const uint16_t* X, const uint16_t* A, int64_t M, int64_t K, int r, uint16_t* V,
+                            cudaStream_t stream, float scale, Dropout drop) {
+  if (M < 1 || M > kGemvMaxTokens) return cudaErrorInvalidValue;
   static bool attr_set[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
   if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(xa_small_kernel<kAct8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(xa_smem_bytes(kAct8)));
+    cudaError_t e = cudaFuncSetAttribute(xa_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kXaSmemBytes));
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(xa_small_kernel<kAct8>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      e = cudaFuncSetAttribute(xa_small_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   int S, Kc;
-  xa_plan(a.K, S, Kc);
-  a.Kc = Kc;
+  xa_plan(K, S, Kc);
+  XaArgs a{X, A, static_cast<int>(M), K, r, Kc, V, scale, drop.keep, drop.keep_scale, drop.ctr};
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.r + kXaCols - 1) / kXaCols), static_cast<unsigned>(S));
+  cfg.gridDim = dim3(static_cast<unsigned>((r + kXaCols - 1) / kXaCols), static_cast<unsigned>(S));
   cfg.blockDim = dim3(kXaThreads);
-  cfg.dynamicSmemBytes = xa_smem_bytes(kAct8);
+  cfg.dynamicSmemBytes = kXaSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -234,25 +214,10 @@ cudaError_t run_xa_small(XaArgs a, cudaStream_t stream) {
   cfg.attrs = at;
   cfg.numAttrs = 2;
   timing_before(QLORA_KERNEL_RANK_R, stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, xa_small_kernel<kAct8>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, xa_small_kernel, a);
   timing_after(QLORA_KERNEL_RANK_R, stream);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_xa_small(const uint16_t* X, const uint16_t* A, int64_t M, int64_t K, int r, uint16_t* V,
-                            cudaStream_t stream, float scale, Dropout drop) {
-  return run_xa_small<false>(XaArgs{X, A, static_cast<int>(M), K, r, 0, V, scale, drop.keep, drop.keep_scale, drop.ctr,
-                                    nullptr, 0}, stream);
-}
-
-cudaError_t launch_xa_small_act(const ActView& x, const uint16_t* A, int64_t M, int64_t K, int r, uint16_t* V,
-                                cudaStream_t stream, float scale) {
-  const XaArgs a{static_cast<const uint16_t*>(x.x), A, static_cast<int>(M), K, r, 0, V, scale, nullptr, 1.0f,
-                 DropoutCounter{}, x.scales, x.block};
-  return x.scales ? run_xa_small<true>(a, stream) : run_xa_small<false>(a, stream);
 }
 
 }  // namespace qlora
