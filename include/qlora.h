@@ -512,8 +512,7 @@ QLORA_API size_t qlora_rmsnorm_ws_bytes(int64_t M, int64_t n);
  *   Y = bf16(X w' + s (X A) B),   V = bf16(s X A),   w' = (code - 8) scale
  * with fp32 accumulation.  Unlike qlora_linear_fwd it does not round w' or the V in
  * Y to bf16 (it rounds the products x scale instead, once, to bf16), and it reads
- * 8-bit activations as qlora_rmsnorm_fwd writes them.  It needs no workspace, and
- * calls on different streams do not touch each other.
+ * 8-bit activations as qlora_rmsnorm_fwd writes them.
  *   w         [host] descriptor; another format is QLORA_ERR_INVALID_ARG.
  *   X         [device] bf16 (M, in), or with x_scales uint8 (M, in) E4M3 codes.
  *   x_scales  [device] fp32 (M, in / 64) for x_block = 64, (M) for x_block = 0:
@@ -523,11 +522,14 @@ QLORA_API size_t qlora_rmsnorm_ws_bytes(int64_t M, int64_t n);
  *   s         adapter_scale, finite.
  *   Y         [device] out: bf16 (M, out).
  *   V_save    [device] out: V, bf16 (M, r), or NULL.
+ *   ws        [device] a workspace of at least 1280 bytes (the prefix), initialised by
+ *             qlora_ws_init; it may be the layer's.  Only its status word is used (for
+ *             a bounded wait that gives up), so calls on several streams may share it.
  * QLORA_ERR_SHAPE unless 1 <= M <= 16, in % 64 == 0 and out % 64 == 0.
  */
 QLORA_API qlora_status qlora_matvec(const qlora_nf4_weight* w, const void* X, const float* x_scales, int x_block,
                                     int64_t M, const uint16_t* A, const uint16_t* B, int r, float adapter_scale,
-                                    uint16_t* Y, uint16_t* V_save, void* stream);
+                                    uint16_t* Y, uint16_t* V_save, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- helpers */
 

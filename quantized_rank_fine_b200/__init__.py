@@ -135,7 +135,7 @@ def lib() -> ctypes.CDLL:
             "qlora_rmsnorm_fwd": (i32, [vp, vp, vp, i32, f32, i64, i64, dp, vp, vp, vp, vp, i32, vp, vp]),
             "qlora_rmsnorm_bwd": (i32, [vp, vp, vp, i32, vp, vp, i64, i64, dp, vp, vp, vp, u32, vp, sz, vp]),
             "qlora_rmsnorm_ws_bytes": (sz, [i64, i64]),
-            "qlora_matvec": (i32, [wp, vp, vp, i32, i64, vp, vp, i32, f32, vp, vp, vp]),
+            "qlora_matvec": (i32, [wp, vp, vp, i32, i64, vp, vp, i32, f32, vp, vp, vp, sz, vp]),
             "qlora_linear_fwd_ex": (i32, [wp, vp, i64, vp, vp, i32, vp, vp, ctypes.POINTER(_LinearOpts), vp, sz,
                                           vp]),
             "qlora_linear_bwd_ex": (i32, [wp, vp, vp, vp, i64, vp, vp, i32, vp, vp, vp,
@@ -646,12 +646,11 @@ def qlora_rmsnorm_bwd(dY: torch.Tensor, H: torch.Tensor, G: torch.Tensor, rstd: 
     return (dR if drop is None else dX), dR, (dG if need_dG else None)
 
 
-def qlora_matvec(w: NF4Weight, X, workspace: Workspace | None = None, A=None, B=None, adapter_scale: float = 1.0,
+def qlora_matvec(w: NF4Weight, X, workspace: Workspace, A=None, B=None, adapter_scale: float = 1.0,
                  save_V: bool = False, stream=None, Y=None, V=None):
     """Up to 16 tokens through an integer weight (int_weight): X is bf16 (M, in) or
     the Act8 that qlora_rmsnorm_fwd returns; A and B the adapters, or None.  Returns
-    (Y, V), V = s X A with save_V and adapters, else None.  The call needs no scratch:
-    `workspace` is accepted, as in the layer's calls, and left alone."""
+    (Y, V), V = s X A with save_V and adapters, else None."""
     bf16 = torch.bfloat16
     scales, block = None, 0
     if isinstance(X, Act8):
@@ -666,16 +665,18 @@ def qlora_matvec(w: NF4Weight, X, workspace: Workspace | None = None, A=None, B=
     if K != w.n_in:
         raise ValueError(f"X has {K} columns, the weight {w.n_in} rows")
     r = 0 if A is None else A.shape[1]
+    a, b = _arg(A, (K, r), bf16), _arg(B, (r, N), bf16)
     if Y is None:
         Y = _empty((M, N), bf16, X.device, stream)
     if not save_V or r == 0:
         V = None
     elif V is None:
         V = _empty((M, r), bf16, X.device, stream)
+    buf = workspace.get(_WS_PREFIX, stream)
     ws = w.c_struct()
-    _check(lib().qlora_matvec(ctypes.byref(ws), x, scales, block, M, _arg(A, (K, r), bf16), _arg(B, (r, N), bf16), r,
-                              adapter_scale, _arg(Y, (M, N), bf16), _arg(V, (M, r), bf16), _stream(stream)),
-           "qlora_matvec")
+    _check(lib().qlora_matvec(ctypes.byref(ws), x, scales, block, M, a, b, r, adapter_scale,
+                              _arg(Y, (M, N), bf16), _arg(V, (M, r), bf16), buf.data_ptr(),
+                              buf.numel(), _stream(stream)), "qlora_matvec")
     return Y, V
 
 

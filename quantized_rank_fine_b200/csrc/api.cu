@@ -719,21 +719,22 @@ qlora_status qlora_rmsnorm_bwd(const uint16_t* dY, const uint16_t* H, const void
 
 qlora_status qlora_matvec(const qlora_nf4_weight* w, const void* X, const float* x_scales, int x_block, int64_t M,
                           const uint16_t* A, const uint16_t* B, int r, float adapter_scale, uint16_t* Y,
-                          uint16_t* V_save, void* stream) {
+                          uint16_t* V_save, void* ws, size_t ws_bytes, void* stream) {
   if (!X || !Y || (r != 0) != (A != nullptr) || (r != 0) != (B != nullptr) || (r == 0 && V_save) ||
       (x_scales && x_block != 0 && x_block != 64) || !std::isfinite(adapter_scale))
     return QLORA_ERR_INVALID_ARG;
   QLORA_TRY(check_weight_shape(w));
   if (w->dq_format != QLORA_FMT_INT16) return QLORA_ERR_INVALID_ARG;
   if (!matvec_shape_ok(M, w->in, w->out, r)) return QLORA_ERR_SHAPE;
+  if (!ws || ws_bytes < kFixedBytes) return QLORA_ERR_WORKSPACE;
   QLORA_TRY(check_device());
   QLORA_TRY(check_weight(w));
-  for (const void* p : {X, static_cast<const void*>(Y)}) QLORA_TRY(check_ptr(p));
+  for (const void* p : {X, static_cast<const void*>(Y), static_cast<const void*>(ws)}) QLORA_TRY(check_ptr(p));
   for (const void* p : {static_cast<const void*>(x_scales), static_cast<const void*>(A), static_cast<const void*>(B),
                         static_cast<const void*>(V_save)})
     QLORA_TRY(check_ptr(p, false));
   QLORA_CUDA(qlora::launch_matvec(view(w), qlora::ActView{X, x_scales, x_block}, A, B, M, r, adapter_scale, Y, V_save,
-                                  static_cast<cudaStream_t>(stream)));
+                                  static_cast<uint32_t*>(ws), static_cast<cudaStream_t>(stream)));
   return QLORA_OK;
 }
 

@@ -144,7 +144,7 @@ struct ActView {
 // Y = X w' + scale (X A) B for an integer weight (kFmtInt16), M <= kGemvMaxTokens;
 // r = 0 leaves the adapter term out; V (M x r) is stored unless nullptr.
 cudaError_t launch_matvec(const WeightView& w, const ActView& x, const uint16_t* A, const uint16_t* B, int64_t M,
-                          int r, float scale, uint16_t* Y, uint16_t* V, cudaStream_t stream);
+                          int r, float scale, uint16_t* Y, uint16_t* V, uint32_t* status, cudaStream_t stream);
 
 // Residual addition and RMS norm (see qlora_rmsnorm_fwd); null pointers leave a
 // part out.  n is a multiple of 8, at most kNormMaxCols.

@@ -78,9 +78,10 @@ def test_rmsnorm_ws_bytes(L):
     assert _bwd(L, nb=nb - 1) == WORKSPACE
 
 
-def _mv(L, w=None, X=FAKE, xs=None, block=0, M=4, A=FAKE, B=FAKE, r=8, s=1.0, Y=FAKE, V=None):
+def _mv(L, w=None, X=FAKE, xs=None, block=0, M=4, A=FAKE, B=FAKE, r=8, s=1.0, Y=FAKE, V=None,
+        ws=FAKE, nb=1 << 30):
     w = w or q._Weight(0x10000, 0, 0x10000, 256, 128, q.QLORA_FMT_INT16)
-    return L.qlora_matvec(ctypes.byref(w), X, xs, block, M, A, B, r, s, Y, V, None)
+    return L.qlora_matvec(ctypes.byref(w), X, xs, block, M, A, B, r, s, Y, V, ws, nb, None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -89,6 +90,7 @@ def _mv(L, w=None, X=FAKE, xs=None, block=0, M=4, A=FAKE, B=FAKE, r=8, s=1.0, Y=
     (dict(xs=FAKE, block=32), INVALID), (dict(w=q._Weight(0x10000, 0x10000, 0x10000, 256, 128, 0)), INVALID),
     (dict(M=0), SHAPE), (dict(M=17), SHAPE), (dict(r=4), SHAPE), (dict(r=12), SHAPE), (dict(r=264), SHAPE),
     (dict(w=q._Weight(0x10000, 0, 0x10000, 256, 96, 2)), SHAPE), (dict(w=q._Weight(0x10000, 0, 0x10000, 32, 64, 2)), SHAPE),
+    (dict(ws=None), WORKSPACE), (dict(nb=1279), WORKSPACE),
 ])
 def test_matvec_rejects(L, kw, want):
     assert _mv(L, **kw) == want
