@@ -461,15 +461,16 @@ QLORA_API qlora_status qlora_loftq_split(const float* U, int64_t ldu, const floa
  *   R        [device] bf16 (M, n), the residual stream, or NULL for none.
  *   G        [device] the gain, n values of g_dtype (QLORA_F32 or QLORA_BF16).
  *   eps      > 0 and finite, else QLORA_ERR_INVALID_ARG.
- *   drop     [host] dropout of X (mask over (M, n)), or NULL.
+ *   drop     [host] dropout of X (mask over (M, n)), or NULL.  A dropped X adds
+ *            nothing, whatever it holds.
  *   H        [device] out: bf16 (M, n), or NULL where it is not wanted.
  *   Y        [device] out: bf16(y) (M, n), or NULL.
  *   Q        [device] out: y in 8 bits, uint8 (M, n) E4M3 codes, or NULL.  Per block
  *            of q_block columns (64, or 0 for the whole row): a = max |y|,
- *            s = fl32(a / 448), code = E4M3(fl32(y / s)) round to nearest even (0
- *            where s = 0), so y ~ code s.  y is not rounded to bf16 in between.  A
- *            block that holds a NaN or an infinity gets codes and a scale whose
- *            products are NaN.
+ *            s = fl32(a / 448) (0 where that is below 2^-126), code =
+ *            E4M3(fl32(y fl32(1 / s))) round to nearest even (0 where s = 0), so
+ *            y ~ code s.  y is not rounded to bf16 in between.  A block that holds a
+ *            NaN or an infinity gets codes and a scale whose products are NaN.
  *   q_scales [device] out: fp32 (M, n / 64), or (M) with q_block = 0.  With Q only.
  *   rstd     [device] out: fp32 (M), for the backward, or NULL.
  * QLORA_ERR_INVALID_ARG without Y and Q, with Q but no q_scales, or for another q_block.

@@ -88,7 +88,7 @@ qlora_status read_dropout(const qlora_dropout* d, qlora::DropoutCounter& c, floa
   if (d->p == 0.0f) return QLORA_OK;
   c.on = 1;
   c.threshold = static_cast<uint32_t>(std::rint(static_cast<double>(d->p) * 4294967296.0));
-  c.seed = d->seed;
+  qlora::philox_keys(d->seed, c.key);
   c.offset = d->offset;
   c.counter = d->counter;
   keep_scale = static_cast<float>(1.0 / (1.0 - static_cast<double>(d->p)));

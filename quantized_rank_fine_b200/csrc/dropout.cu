@@ -13,14 +13,14 @@ namespace {
 
 constexpr int kDmThreads = 256;
 
-__global__ void __launch_bounds__(kDmThreads) dropout_mask_kernel(DropoutCounter d, int64_t n, uint8_t* keep) {
+__global__ void __launch_bounds__(kDmThreads) dropout_mask_kernel(const __grid_constant__ DropoutCounter d, int64_t n, uint8_t* keep) {
   const int64_t e0 = (static_cast<int64_t>(blockIdx.x) * kDmThreads + threadIdx.x) * 16;
   if (e0 >= n) return;
   const uint64_t off = dropout_offset(d);
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint4 u = philox4x32_10(static_cast<uint64_t>(e0 / 4 + i), off, d.seed);
+    const uint4 u = philox4x32_10(static_cast<uint64_t>(e0 / 4 + i), off, d);
     w[i] = (u.x >= d.threshold ? 1u : 0u) | (u.y >= d.threshold ? 0x100u : 0u) |
            (u.z >= d.threshold ? 0x10000u : 0u) | (u.w >= d.threshold ? 0x1000000u : 0u);
   }
@@ -32,6 +32,13 @@ __global__ void __launch_bounds__(kDmThreads) dropout_mask_kernel(DropoutCounter
 }
 
 }  // namespace
+
+void philox_keys(uint64_t seed, uint32_t (&key)[20]) {
+  for (uint32_t i = 0; i < 10; ++i) {
+    key[2 * i] = static_cast<uint32_t>(seed) + i * 0x9E3779B9u;
+    key[2 * i + 1] = static_cast<uint32_t>(seed >> 32) + i * 0xBB67AE85u;
+  }
+}
 
 cudaError_t launch_dropout_mask(const DropoutCounter& d, int64_t n, uint8_t* keep, cudaStream_t stream) {
   const int64_t grid = (n + kDmThreads * 16 - 1) / (kDmThreads * 16);

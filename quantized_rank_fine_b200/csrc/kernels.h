@@ -99,7 +99,7 @@ struct AdamParams {
 struct DropoutCounter {
   int on = 0;
   uint32_t threshold = 0;
-  uint64_t seed = 0;
+  uint32_t key[20] = {};               // the round keys k0, k1 of the seed (philox_keys)
   uint64_t offset = 0;
   const uint64_t* counter = nullptr;   // device, added to offset; may be nullptr
 };
@@ -108,6 +108,7 @@ struct Dropout {
   float keep_scale = 1.0f;
   DropoutCounter ctr;
 };
+void philox_keys(uint64_t seed, uint32_t (&key)[20]);
 // The counter's mask of n elements as bytes (1 = keep); keep 16-byte aligned.
 cudaError_t launch_dropout_mask(const DropoutCounter& d, int64_t n, uint8_t* keep, cudaStream_t stream);
 cudaError_t launch_xa(const uint16_t* X, const uint16_t* A, int64_t M, int64_t n_in, int r, uint16_t* V,

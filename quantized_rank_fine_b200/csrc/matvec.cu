@@ -19,7 +19,7 @@
 //     The byte transpose of ldmatrix (m16n16 .b8) hands lane (g, t) one byte, two
 //     columns, of four rows; a byte permute sets the nibble into bf16 128 + code
 //     and one packed subtraction of 136 leaves q.
-//   * x s is rounded to bf16 (2^-9 of each product at most, signs independent), the
+//   * x s is rounded to bf16 (2^-8 of each product at most, signs independent), the
 //     same size as the output's own rounding; sums are fp32.  x itself and V are not
 //     rounded in a way that reaches Y: V goes in as a sum of two bf16 numbers.
 #include "common.cuh"

@@ -13,20 +13,18 @@
 
 namespace qlora {
 
-__device__ __forceinline__ uint4 philox4x32_10(uint64_t block, uint64_t offset, uint64_t seed) {
+// The round keys come with the launch (they depend on the seed alone), so a round is
+// two wide products and two three-way exclusive ors.
+__device__ __forceinline__ uint4 philox4x32_10(uint64_t block, uint64_t offset, const DropoutCounter& d) {
   uint32_t x0 = static_cast<uint32_t>(block), x1 = static_cast<uint32_t>(block >> 32);
   uint32_t x2 = static_cast<uint32_t>(offset), x3 = static_cast<uint32_t>(offset >> 32);
-  uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
     const uint64_t a = static_cast<uint64_t>(0xD2511F53u) * x0, b = static_cast<uint64_t>(0xCD9E8D57u) * x2;
-    const uint32_t y0 = static_cast<uint32_t>(b >> 32) ^ x1 ^ k0, y2 = static_cast<uint32_t>(a >> 32) ^ x3 ^ k1;
+    x0 = static_cast<uint32_t>(b >> 32) ^ x1 ^ d.key[2 * i];
+    x2 = static_cast<uint32_t>(a >> 32) ^ x3 ^ d.key[2 * i + 1];
     x1 = static_cast<uint32_t>(b);
     x3 = static_cast<uint32_t>(a);
-    x0 = y0;
-    x2 = y2;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   return make_uint4(x0, x1, x2, x3);
 }

@@ -3,20 +3,26 @@
 //
 //   h = bf16(res + keep x / (1 - p)),  rstd = 1 / sqrt(mean(h^2) + eps),  y = h rstd g
 //   out: h (bf16), bf16(y), and y in 8 bits: per row or per 64 columns
-//        s = fl32(max|y| / 448), code = E4M3(fl32(y / s))
+//        s = fl32(max|y| / 448), code = E4M3(fl32(y fl32(1 / s)))
 //   gh = g dy,  c = mean(gh h) rstd^2,  dh = rstd (gh - h c) + dH
 //   out: dR = bf16(dh), dX = bf16(keep dh / (1 - p)), dG = sum over rows of dy h rstd
 //
 // Both are bound by streaming the rows once (a few flops and bytes an element).
 // A CTA takes a row: every thread holds its 16-byte vectors of the row in
 // registers, so the row is read once however many passes the arithmetic takes.
+// The gradient's CTAs walk several rows with the next row's loads in flight, and
+// keep their columns of the gain and of its gradient in registers; the parts of
+// the CTAs are added by a second, programmatically dependent launch.
 #include "common.cuh"
 #include "kernels.h"
 #include "philox.cuh"
+#include "sm100.cuh"
 
 namespace qlora {
 
 namespace {
+
+using namespace sm100;
 
 constexpr int kNormMaxThreads = 1024;
 
@@ -51,32 +57,31 @@ __device__ __forceinline__ void load_gain(const void* G, bool f32, int v, float 
   }
 }
 
-// keep * scale of the eight elements from e (a multiple of 8).
-__device__ __forceinline__ void keep8(const DropoutCounter& d, uint64_t off, float scale, int64_t e, float (&f)[8]) {
+// The random words of the eight elements from e (a multiple of 8).
+__device__ __forceinline__ void words8(const DropoutCounter& d, uint64_t off, int64_t e, uint32_t (&u)[8]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint4 u = philox4x32_10(static_cast<uint64_t>(e / 4 + i), off, d.seed);
-    f[4 * i] = u.x >= d.threshold ? scale : 0.0f;
-    f[4 * i + 1] = u.y >= d.threshold ? scale : 0.0f;
-    f[4 * i + 2] = u.z >= d.threshold ? scale : 0.0f;
-    f[4 * i + 3] = u.w >= d.threshold ? scale : 0.0f;
+    const uint4 w = philox4x32_10(static_cast<uint64_t>(e / 4 + i), off, d);
+    u[4 * i] = w.x;
+    u[4 * i + 1] = w.y;
+    u[4 * i + 2] = w.z;
+    u[4 * i + 3] = w.w;
   }
 }
 
-// res + x k, ready to be rounded to bf16.  A binary32 sum that is a tie between two
-// bf16 values may stand for an exact sum on either side of it, and under dropout
-// many do (x / (1 - p) often lies within 2^-26 of a short number): such a sum is
-// formed again in 64 bits and moved off the tie, so that the stored h is the
-// nearest bf16 to the exact sum.  A sum that is not a tie cannot be on the wrong
-// side of one, as ties are binary32 numbers and rounding is monotone.
-__device__ __forceinline__ float add_kept(float res, float x, float k) {
-  float s = fmaf(x, k, res);
-  if ((__float_as_uint(s) & 0xFFFFu) == 0x8000u) {
-    const double t = static_cast<double>(x) * static_cast<double>(k) + static_cast<double>(res);
-    const double sd = static_cast<double>(s);
-    if (t != sd) s = __uint_as_float(__float_as_uint(s) + (((t > sd) == (s > 0.0f)) ? 1u : 0xFFFFFFFFu));
+// res + x scale of eight kept elements (res of the dropped ones, whatever x holds),
+// ready to be rounded to bf16: the sum is rounded to odd in binary32 (of its two
+// neighbours the one with an odd last bit, where it is not exact), so that the second
+// rounding sees on which side of a tie between two bf16 values it lies.  Under dropout
+// many sums lie next to one: x / (1 - p) is often within 2^-26 of a short number.
+__device__ __forceinline__ void add_kept8(const float (&res)[8], const float (&x)[8], const uint32_t (&u)[8],
+                                          uint32_t threshold, float scale, float (&s)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float lo = __fmaf_rd(x[j], scale, res[j]), hi = __fmaf_ru(x[j], scale, res[j]);
+    const float odd = (__float_as_uint(lo) & 1u) ? lo : hi;
+    s[j] = u[j] >= threshold ? odd : res[j];
   }
-  return s;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -117,99 +122,153 @@ __device__ __forceinline__ uint32_t max_bits8(const float (&y)[8]) {
   return a;
 }
 
-__device__ __forceinline__ uint2 e4m3_codes(const float (&y)[8], float s) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float2 q = make_float2(0.0f, 0.0f);
-    if (s != 0.0f) q = make_float2(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s));
-    w[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
-  }
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
+
+// The scale of a block whose largest |y| has these bits, zero below the normal numbers.
+__device__ __forceinline__ float block_scale(uint32_t top) {
+  const float s = __fdiv_rn(__uint_as_float(top), 448.0f);
+  return s < 0x1p-126f ? 0.0f : s;
+}
+
+// E4M3(fl32(y fl32(1 / s))) of eight values, 0 where s = 0.
+__device__ __forceinline__ uint2 e4m3_codes(const float (&y)[8], float s) {
+  if (s == 0.0f) return make_uint2(0u, 0u);
+  const float inv = __frcp_rn(s);
+  return make_uint2(e4m3_pair(y[0] * inv, y[1] * inv) | (e4m3_pair(y[2] * inv, y[3] * inv) << 16),
+                    e4m3_pair(y[4] * inv, y[5] * inv) | (e4m3_pair(y[6] * inv, y[7] * inv) << 16));
+}
+
+// bf16(a + b) of pairs, one rounding.
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// (a.x b.x, a.y b.y) as one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmul.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// A thread's vectors of the row between the passes: as fp32 where they are few (they
+// are unpacked once), as bf16 pairs where they are many.
+template <int VPT, bool kWide>
+struct Held;
+template <int VPT>
+struct Held<VPT, true> {
+  float f[VPT][8];
+  __device__ __forceinline__ void set(int i, uint4, const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[i][j] = v[j];
+  }
+  __device__ __forceinline__ void get(int i, float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = f[i][j];
+  }
+};
+template <int VPT>
+struct Held<VPT, false> {
+  uint4 p[VPT];
+  __device__ __forceinline__ void set(int i, uint4 v, const float (&)[8]) { p[i] = v; }
+  __device__ __forceinline__ void get(int i, float (&v)[8]) const { unpack8(p[i], v); }
+};
 
 // VPT vectors of 8 columns a thread; kQuant: 0 none, 1 one scale a row, 2 one per 64 columns.
 template <int VPT, bool kDrop, int kQuant>
-__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_fwd_kernel(const NormFwd p) {
+__global__ void __launch_bounds__(VPT == 2 ? 512 : kNormMaxThreads) rmsnorm_fwd_kernel(const __grid_constant__ NormFwd p) {
   __shared__ float red[32];
+  grid_launch_dependents();   // they wait for this kernel to finish, as it waits for the one before
+  grid_dependency_wait();
   const int64_t row = blockIdx.x;
   const int nv = static_cast<int>(p.n / 8);
   const uint4* X = reinterpret_cast<const uint4*>(p.X + row * p.n);
   const uint4* R = p.R ? reinterpret_cast<const uint4*>(p.R + row * p.n) : nullptr;
   const uint64_t off = kDrop ? dropout_offset(p.drop) : 0;
-  uint4 h[VPT];
+  Held<VPT, (VPT <= 2)> held;
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
-    h[i] = make_uint4(0u, 0u, 0u, 0u);
+    float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    uint4 h = make_uint4(0u, 0u, 0u, 0u);
     if (v < nv) {
-      h[i] = X[v];
-      float x[8], f[8];
-      unpack8(h[i], x);
-      if (kDrop || R) {
-        float res[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        if (R) unpack8(R[v], res);
-        if (kDrop) {
-          float k[8];
-          keep8(p.drop, off, p.keep_scale, row * p.n + 8 * v, k);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = add_kept(res[j], x[j], k[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = res[j] + x[j];
-        }
-        h[i] = pack8(f);
-        if (p.H) reinterpret_cast<uint4*>(p.H + row * p.n)[v] = h[i];
-        unpack8(h[i], x);
-      } else if (p.H) {
-        reinterpret_cast<uint4*>(p.H + row * p.n)[v] = h[i];
+      h = X[v];
+      uint4 r = make_uint4(0u, 0u, 0u, 0u);
+      if (R) r = R[v];
+      if constexpr (kDrop) {
+        float res[8], s[8];
+        uint32_t u[8];
+        unpack8(h, x);
+        unpack8(r, res);
+        words8(p.drop, off, row * p.n + 8 * v, u);
+        add_kept8(res, x, u, p.drop.threshold, p.keep_scale, s);
+        h = pack8(s);
+      } else if (R) {
+        h = make_uint4(add_bf16x2(h.x, r.x), add_bf16x2(h.y, r.y), add_bf16x2(h.z, r.z), add_bf16x2(h.w, r.w));
       }
+      if (p.H) reinterpret_cast<uint4*>(p.H + row * p.n)[v] = h;
+      unpack8(h, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
     }
+    held.set(i, h, x);
   }
   const float mean = __fdiv_rn(block_sum(ss, red), static_cast<float>(p.n));
   const float rstd = __frsqrt_rn(mean + p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
 
+  // y of a vector, (h rstd) g
+  auto normed = [&](int i, int v, float (&y)[8]) {
+    float h[8], g[8];
+    held.get(i, h);
+    load_gain(p.G, p.g_f32, v, g);
+    const float2 rr = make_float2(rstd, rstd);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float2 o = mul2(mul2(make_float2(h[j], h[j + 1]), rr), make_float2(g[j], g[j + 1]));
+      y[j] = o.x;
+      y[j + 1] = o.y;
+    }
+  };
   uint32_t top = 0;
-  if (kQuant == 1) {
+  if constexpr (kQuant == 1) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v < nv) {
-        float x[8], g[8];
-        unpack8(h[i], x);
-        load_gain(p.G, p.g_f32, v, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = x[j] * rstd * g[j];
-        top = max(top, max_bits8(x));
+        float y[8];
+        normed(i, v, y);
+        if constexpr (VPT <= 2) held.set(i, make_uint4(0u, 0u, 0u, 0u), y);   // y takes the place of h
+        top = max(top, max_bits8(y));
       }
     }
     top = block_max(top, reinterpret_cast<uint32_t*>(red));
-    if (threadIdx.x == 0) p.q_scales[row] = __fdiv_rn(__uint_as_float(top), 448.0f);
+    if (threadIdx.x == 0) p.q_scales[row] = block_scale(top);
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (v < nv) {
-      float g[8];
-      unpack8(h[i], y);
-      load_gain(p.G, p.g_f32, v, g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = y[j] * rstd * g[j];
+      if constexpr (kQuant == 1 && VPT <= 2) held.get(i, y);
+      else normed(i, v, y);
       if (p.Y) reinterpret_cast<uint4*>(p.Y + row * p.n)[v] = pack8(y);
     }
-    if (kQuant == 2) {
+    if constexpr (kQuant == 2) {
       // a block of 64 columns is 8 neighbouring lanes (n is a multiple of 64)
       top = max_bits8(y);
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     }
     if (kQuant && v < nv) {
-      const float s = __fdiv_rn(__uint_as_float(top), 448.0f);
+      const float s = block_scale(top);
       reinterpret_cast<uint2*>(p.Q + row * p.n)[v] = e4m3_codes(y, s);
       if (kQuant == 2 && (v & 7) == 0) p.q_scales[row * (p.n / 64) + v / 8] = s;
     }
@@ -219,59 +278,85 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_fwd_kernel(const Norm
 // One CTA walks the rows blockIdx.x, + gridDim.x, ...; the gain's gradient of a
 // thread's columns stays in registers over them and goes to the CTA's row of `parts`.
 template <int VPT, bool kDrop>
-__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_bwd_kernel(const NormBwd p) {
-  __shared__ float red[32];
-  const int nv = static_cast<int>(p.n / 8);
+__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_bwd_kernel(const __grid_constant__ NormBwd p) {
+  __shared__ float red[2][32];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int nv = static_cast<int>(p.n / 8), nw = blockDim.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t off = kDrop ? dropout_offset(p.drop) : 0;
-  float dg[VPT][8];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dg[i][j] = 0.0f;
-  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
-    const float rstd = p.rstd[row];
-    uint4 h[VPT], dy[VPT];
-    float c = 0.0f;
+  const float cols = static_cast<float>(p.n);
+  float dg[VPT][8], g[VPT][8];
+  uint4 h[VPT], dy[VPT], dh[VPT];
+  float rstd = 0.0f;
+  auto load = [&](int64_t row) {
+    rstd = p.rstd[row];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v < nv) {
         h[i] = reinterpret_cast<const uint4*>(p.H + row * p.n)[v];
         dy[i] = reinterpret_cast<const uint4*>(p.dY + row * p.n)[v];
-        float x[8], d[8], g[8];
-        unpack8(h[i], x);
-        unpack8(dy[i], d);
-        load_gain(p.G, p.g_f32, v, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          c = fmaf(d[j] * g[j], x[j], c);
-          dg[i][j] = fmaf(d[j], x[j] * rstd, dg[i][j]);
-        }
+        if (p.dH) dh[i] = reinterpret_cast<const uint4*>(p.dH + row * p.n)[v];
       }
     }
-    c = __fdiv_rn(block_sum(c, red), static_cast<float>(p.n)) * rstd * rstd;
+  };
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    h[i] = dy[i] = dh[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[i][j] = g[i][j] = 0.0f;
+    if (v < nv) load_gain(p.G, p.g_f32, v, g[i]);
+  }
+  int flip = 0;
+  load(blockIdx.x);
+  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, flip ^= 1) {
+    const float rs = rstd;
+    uint4 x4[VPT], d4[VPT], e4[VPT];
+    float c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      x4[i] = h[i];
+      d4[i] = dy[i];
+      e4[i] = dh[i];
+      float x[8], d[8];
+      unpack8(x4[i], x);
+      unpack8(d4[i], d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        c = fmaf(d[j] * g[i][j], x[j], c);
+        dg[i][j] = fmaf(d[j], x[j] * rs, dg[i][j]);
+      }
+    }
+    if (row + gridDim.x < p.M) load(row + gridDim.x);
+    // two sets of warp sums in turn: a row's are not written before every thread has
+    // read those of the row before the last
+    c = warp_sum(c);
+    if (lane == 0) red[flip][warp] = c;
+    __syncthreads();
+    c = __fdiv_rn(warp_sum(lane < nw ? red[flip][lane] : 0.0f), cols) * rs * rs;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v < nv) {
-        float x[8], d[8], g[8];
-        unpack8(h[i], x);
-        unpack8(dy[i], d);
-        load_gain(p.G, p.g_f32, v, g);
+        float x[8], d[8];
+        unpack8(x4[i], x);
+        unpack8(d4[i], d);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = rstd * fmaf(-c, x[j], d[j] * g[j]);
+        for (int j = 0; j < 8; ++j) d[j] = rs * fmaf(-c, x[j], d[j] * g[i][j]);
         if (p.dH) {
           float e[8];
-          unpack8(reinterpret_cast<const uint4*>(p.dH + row * p.n)[v], e);
+          unpack8(e4[i], e);
 #pragma unroll
           for (int j = 0; j < 8; ++j) d[j] += e[j];
         }
         reinterpret_cast<uint4*>(p.dR + row * p.n)[v] = pack8(d);
         if (kDrop && p.dX) {
-          float k[8];
-          keep8(p.drop, off, p.keep_scale, row * p.n + 8 * v, k);
+          uint32_t u[8];
+          words8(p.drop, off, row * p.n + 8 * v, u);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] *= k[j];
+          for (int j = 0; j < 8; ++j) d[j] = u[j] >= p.drop.threshold ? d[j] * p.keep_scale : 0.0f;
           reinterpret_cast<uint4*>(p.dX + row * p.n)[v] = pack8(d);
         }
       }
@@ -290,43 +375,96 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_bwd_kernel(const Norm
   }
 }
 
-// dG[col] = the sum of the parts in CTA order (the same bits every time).
-__global__ void __launch_bounds__(256) rmsnorm_dgain_kernel(const float* parts, int nparts, int64_t n, float* dG,
+// dG[col] = the sum of the parts.  A CTA takes 32 columns (8 threads of 4): row lane l
+// of 32 adds the parts l, l + 32, ..., and the lanes are added in order, so the bits
+// are the same every time.
+__global__ void __launch_bounds__(256) rmsnorm_dgain_kernel(const float4* parts, int nparts, int64_t n, float4* dG,
                                                             int accumulate) {
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (col >= n) return;
-  float s = 0.0f;
-  for (int i = 0; i < nparts; ++i) s += parts[i * n + col];
-  dG[col] = accumulate ? dG[col] + s : s;
+  __shared__ float4 red[32][8];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int c = threadIdx.x & 7, l = threadIdx.x >> 3;
+  const int64_t nq = n / 4, q = static_cast<int64_t>(blockIdx.x) * 8 + c;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (q < nq) {
+#pragma unroll 8
+    for (int i = l; i < nparts; i += 32) {
+      const float4 v = __ldcg(parts + i * nq + q);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+  }
+  red[l][c] = s;
+  __syncthreads();
+  if (threadIdx.x >= 8 || q >= nq) return;
+  s = accumulate ? dG[q] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float4 v = red[i][c];
+    t.x += v.x;
+    t.y += v.y;
+    t.z += v.z;
+    t.w += v.w;
+  }
+  dG[q] = make_float4(s.x + t.x, s.y + t.y, s.z + t.z, s.w + t.w);
 }
 
 constexpr int kNormParts = 296;   // most CTAs of the gradient (two per SM)
 
-// Vectors a thread holds and the threads of a CTA for rows of nv vectors.
-void norm_plan(int64_t nv, int& vpt, int& threads) {
+// Launch as a programmatic dependent (the kernels wait before they touch memory).
+template <typename... P, typename... A>
+void launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, args...);   // a failure is the last error, read by the caller
+}
+
+// Vectors a thread holds and the threads of a CTA for rows of nv vectors.  Forward:
+// one vector a thread while there are fewer rows than would fill the SMs (a row's
+// latency counts: 1 x 4096, 2.6 us against 3.4 with two), else two (2048 x 4096, 10.8
+// us against 12.9: twice the CTAs lie on an SM); more only where a row has more than a
+// CTA's threads hold.
+void fwd_plan(int64_t M, int64_t nv, int& vpt, int& threads) {
+  vpt = M < 592 && nv <= 1024 ? 1 : (nv <= 1024 ? 2 : (nv <= 4096 ? 4 : 8));
+  threads = static_cast<int>(((nv + vpt - 1) / vpt + 31) / 32 * 32);
+}
+
+// Gradient: a thread keeps 16 floats of gain and its gradient a vector, so one vector
+// a thread as far as 1024 threads go; a row of more than 8192 columns spills.
+void bwd_plan(int64_t nv, int& vpt, int& threads) {
   vpt = nv <= 1024 ? 1 : (nv <= 2048 ? 2 : (nv <= 4096 ? 4 : 8));
   threads = static_cast<int>(((nv + vpt - 1) / vpt + 31) / 32 * 32);
 }
 
 template <int VPT>
 void run_fwd(const NormFwd& a, int threads, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.M));
+  const unsigned grid = static_cast<unsigned>(a.M);
   const int quant = a.Q ? (a.q_block ? 2 : 1) : 0;
   if (a.drop.on) {
-    if (quant == 0) rmsnorm_fwd_kernel<VPT, true, 0><<<grid, threads, 0, stream>>>(a);
-    else if (quant == 1) rmsnorm_fwd_kernel<VPT, true, 1><<<grid, threads, 0, stream>>>(a);
-    else rmsnorm_fwd_kernel<VPT, true, 2><<<grid, threads, 0, stream>>>(a);
+    if (quant == 0) launch_dependent(rmsnorm_fwd_kernel<VPT, true, 0>, grid, threads, stream, a);
+    else if (quant == 1) launch_dependent(rmsnorm_fwd_kernel<VPT, true, 1>, grid, threads, stream, a);
+    else launch_dependent(rmsnorm_fwd_kernel<VPT, true, 2>, grid, threads, stream, a);
   } else {
-    if (quant == 0) rmsnorm_fwd_kernel<VPT, false, 0><<<grid, threads, 0, stream>>>(a);
-    else if (quant == 1) rmsnorm_fwd_kernel<VPT, false, 1><<<grid, threads, 0, stream>>>(a);
-    else rmsnorm_fwd_kernel<VPT, false, 2><<<grid, threads, 0, stream>>>(a);
+    if (quant == 0) launch_dependent(rmsnorm_fwd_kernel<VPT, false, 0>, grid, threads, stream, a);
+    else if (quant == 1) launch_dependent(rmsnorm_fwd_kernel<VPT, false, 1>, grid, threads, stream, a);
+    else launch_dependent(rmsnorm_fwd_kernel<VPT, false, 2>, grid, threads, stream, a);
   }
 }
 
 template <int VPT>
 void run_bwd(const NormBwd& a, int grid, int threads, cudaStream_t stream) {
-  if (a.drop.on) rmsnorm_bwd_kernel<VPT, true><<<grid, threads, 0, stream>>>(a);
-  else rmsnorm_bwd_kernel<VPT, false><<<grid, threads, 0, stream>>>(a);
+  if (a.drop.on) launch_dependent(rmsnorm_bwd_kernel<VPT, true>, grid, threads, stream, a);
+  else launch_dependent(rmsnorm_bwd_kernel<VPT, false>, grid, threads, stream, a);
 }
 
 int bwd_grid(int64_t M) { return static_cast<int>(std::min<int64_t>(M, kNormParts)); }
@@ -337,7 +475,7 @@ size_t norm_bwd_parts_bytes(int64_t M, int64_t n) { return static_cast<size_t>(b
 
 cudaError_t launch_rmsnorm_fwd(const NormFwd& a, cudaStream_t stream) {
   int vpt, threads;
-  norm_plan(a.n / 8, vpt, threads);
+  fwd_plan(a.M, a.n / 8, vpt, threads);
   timing_before(QLORA_KERNEL_RMSNORM, stream);
   if (vpt == 1) run_fwd<1>(a, threads, stream);
   else if (vpt == 2) run_fwd<2>(a, threads, stream);
@@ -350,7 +488,7 @@ cudaError_t launch_rmsnorm_fwd(const NormFwd& a, cudaStream_t stream) {
 
 cudaError_t launch_rmsnorm_bwd(const NormBwd& a, cudaStream_t stream) {
   int vpt, threads;
-  norm_plan(a.n / 8, vpt, threads);
+  bwd_plan(a.n / 8, vpt, threads);
   const int grid = bwd_grid(a.M);
   timing_before(QLORA_KERNEL_RMSNORM_BWD, stream);
   if (vpt == 1) run_bwd<1>(a, grid, threads, stream);
@@ -360,8 +498,9 @@ cudaError_t launch_rmsnorm_bwd(const NormBwd& a, cudaStream_t stream) {
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && a.dG) {
-    rmsnorm_dgain_kernel<<<static_cast<unsigned>((a.n + 255) / 256), 256, 0, stream>>>(a.parts, grid, a.n, a.dG,
-                                                                                      a.accumulate ? 1 : 0);
+    launch_dependent(rmsnorm_dgain_kernel, static_cast<unsigned>((a.n + 31) / 32), 256, stream,
+                     reinterpret_cast<const float4*>(a.parts), grid, a.n, reinterpret_cast<float4*>(a.dG),
+                     a.accumulate ? 1 : 0);
     count_launch();
     e = cudaGetLastError();
   }

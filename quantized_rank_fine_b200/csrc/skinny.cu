@@ -97,7 +97,7 @@ __device__ __forceinline__ void store_pair(const SkArgs& p, int64_t row, int col
     } else if (p.ctr.on) {
       // r and col are even, so the pair is words 0, 1 or 2, 3 of one Philox block
       const int64_t e = row * p.r + col;
-      const uint4 u = philox4x32_10(static_cast<uint64_t>(e >> 2), dropout_offset(p.ctr), p.ctr.seed);
+      const uint4 u = philox4x32_10(static_cast<uint64_t>(e >> 2), dropout_offset(p.ctr), p.ctr);
       v0 *= ((e & 2) ? u.z : u.x) >= p.ctr.threshold ? p.keep_scale : 0.0f;
       v1 *= ((e & 2) ? u.w : u.y) >= p.ctr.threshold ? p.keep_scale : 0.0f;
     }

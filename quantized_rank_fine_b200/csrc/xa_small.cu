@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kXaThreads) xa_small_kernel(const XaArgs p) {
     if (p.keep) {
       v *= p.keep[at] ? p.keep_scale : 0.0f;
     } else if (p.ctr.on) {
-      const uint4 u = philox4x32_10(static_cast<uint64_t>(at >> 2), dropout_offset(p.ctr), p.ctr.seed);
+      const uint4 u = philox4x32_10(static_cast<uint64_t>(at >> 2), dropout_offset(p.ctr), p.ctr);
       const uint32_t word = (at & 2) ? ((at & 1) ? u.w : u.z) : ((at & 1) ? u.y : u.x);
       v *= word >= p.ctr.threshold ? p.keep_scale : 0.0f;
     }

@@ -119,18 +119,31 @@ def test_zero_rows_and_nonfinite_values():
 
 
 def test_tiny_blocks_quantise():
-    """Blocks of very small values: scales down to subnormals, no NaN."""
+    """Blocks of very small values: a scale that would be subnormal is zero, and so is
+    the block; a small normal one quantises as any other.  No NaN."""
     n = 128
     g = torch.full((n,), 1e-30, device="cuda")
     g[64:] = 2.0 ** -140
     x = _inputs(2, n)["x"]
     o = q.qlora_rmsnorm_fwd(x, g, EPS, want_y=False, quant_block=64)
     v = _np(o.act.codes.view(torch.float8_e4m3fn).float())
-    assert np.isfinite(v).all()
     _, y, _ = norm.rmsnorm(_np(x), None, _np(g), EPS)
-    s = np.repeat(_np(o.act.scales), 64, axis=1)
-    # a scale next to 2^-149 is itself off by half a step of 2^-149, 448 of them at the largest code
-    assert np.all(np.abs(v * s - y) <= 2.0 ** -3 * np.abs(y) + s * 2.0 ** -9 + 225 * 2.0 ** -149)
+    s = _np(o.act.scales)
+    assert np.count_nonzero(v[:, 64:]) == 0 and np.count_nonzero(s[:, 1]) == 0 and np.all(s[:, 0] > 0)
+    assert np.all(np.abs(v[:, :64] * s[:, :1] - y[:, :64]) <= (2.0 ** -4 + 2.0 ** -15) * np.abs(y[:, :64]) + s[:, :1] * 2.0 ** -9)
+
+
+def test_dropped_values_do_not_count():
+    """NaN and infinity at dropped places of the branch leave every output finite."""
+    M, n, p = 8, 512, 0.5
+    d = _inputs(M, n, 12)
+    drop = q.Dropout(p, 3, 4)
+    keep = torch.from_numpy(norm.keep_mask(p, 3, 4, M, n)).cuda()
+    bad = torch.where(keep, d["x"], torch.tensor(float("nan"), dtype=BF, device="cuda"))
+    bad[:, ::3] = torch.where(keep[:, ::3], bad[:, ::3], torch.tensor(float("inf"), dtype=BF, device="cuda"))
+    a = q.qlora_rmsnorm_fwd(bad, d["g"], EPS, d["res"], drop, quant_block=64)
+    b = q.qlora_rmsnorm_fwd(d["x"], d["g"], EPS, d["res"], drop, quant_block=64)
+    assert torch.equal(a.H, b.H) and torch.equal(a.Y, b.Y) and torch.equal(a.act.codes, b.act.codes)
 
 
 @pytest.mark.parametrize("M,n", SHAPES)
