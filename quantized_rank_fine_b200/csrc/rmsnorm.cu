@@ -40,6 +40,24 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
+// Two fp32 operations as one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmul.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%6, %7};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // The gain of columns 8v .. 8v+7.
 __device__ __forceinline__ void load_gain(const void* G, bool f32, int v, float (&g)[8]) {
   if (f32) {
@@ -144,16 +162,6 @@ __device__ __forceinline__ uint2 e4m3_codes(const float (&y)[8], float s) {
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// (a.x b.x, a.y b.y) as one instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmul.rn.f32x2 p, p, q;\n\t"
-      "mov.b64 {%0, %1}, p;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
 
@@ -275,120 +283,163 @@ __global__ void __launch_bounds__(VPT == 2 ? 512 : kNormMaxThreads) rmsnorm_fwd_
   }
 }
 
-// One CTA walks the rows blockIdx.x, + gridDim.x, ...; the gain's gradient of a
-// thread's columns stays in registers over them and goes to the CTA's row of `parts`.
-template <int VPT, bool kDrop>
-__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_bwd_kernel(const __grid_constant__ NormBwd p) {
-  __shared__ float red[2][32];
+constexpr int kBwdThreads = 512;    // of a CTA that takes several short rows at once
+constexpr int kBwdMaxCluster = 8;   // CTAs that share a row of more than 8192 columns
+
+struct BwdPlan {
+  int threads;    // a row's threads in a CTA, one vector of 8 columns each
+  int groups;     // rows a CTA takes at once
+  int cluster;    // CTAs that share a row
+  int ctas;       // CTAs (or clusters), each with its row of `parts`
+};
+
+// Threads for one vector each: a short row leaves room for several in a CTA of 512
+// threads (two CTAs an SM), a row of up to 8192 columns has a CTA to itself, and a
+// longer one is split over a cluster (one CTA an SM).
+BwdPlan bwd_plan(int64_t M, int64_t n) {
+  const int nv = static_cast<int>(n / 8);
+  BwdPlan b{};
+  b.cluster = nv <= 1024 ? 1 : (nv <= 2048 ? 2 : (nv <= 4096 ? 4 : 8));
+  b.threads = ((nv + b.cluster - 1) / b.cluster + 31) / 32 * 32;
+  b.groups = b.threads <= kBwdThreads / 2 ? kBwdThreads / b.threads : 1;
+  const int64_t most = b.threads <= kBwdThreads ? 296 : 148 / b.cluster;
+  b.ctas = static_cast<int>(std::min<int64_t>((M + b.groups - 1) / b.groups, most));
+  return b;
+}
+
+// A group of `threads` threads walks the rows blockIdx.x groups + its number, ... (a
+// cluster of kCluster CTAs the rows of its own number), one vector a thread, with the
+// next row's loads in flight; the gain's gradient of a thread's columns stays in
+// registers and goes to the CTA's row of `parts`.
+template <bool kDrop, bool kCluster>
+__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_bwd_kernel(const __grid_constant__ NormBwd p,
+                                                                      const int threads, const int groups) {
+  __shared__ float red[2][kCluster ? 32 * kBwdMaxCluster : 32];
+  __shared__ float4 sums[kCluster ? 1 : kBwdThreads * 2];
   grid_launch_dependents();
   grid_dependency_wait();
-  const int nv = static_cast<int>(p.n / 8), nw = blockDim.x >> 5;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = threads >> 5;
+  const int group = kCluster ? 0 : threadIdx.x / threads;
+  const int C = kCluster ? static_cast<int>(cluster_nctarank()) : 1, rank = kCluster ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t step = kCluster ? gridDim.x / C : static_cast<int64_t>(gridDim.x) * groups;
+  const int64_t first = kCluster ? blockIdx.x / C : static_cast<int64_t>(blockIdx.x) * groups;
+  const int v = rank * threads + threadIdx.x - group * threads;   // vector of the row
+  const bool mine = v < static_cast<int>(p.n / 8);
   const uint64_t off = kDrop ? dropout_offset(p.drop) : 0;
   const float cols = static_cast<float>(p.n);
-  float dg[VPT][8], g[VPT][8];
-  uint4 h[VPT], dy[VPT], dh[VPT];
-  float rstd = 0.0f;
+  float dg[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, g[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  uint4 h, dy, dh;
+  float rstd;
   auto load = [&](int64_t row) {
-    rstd = p.rstd[row];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < nv) {
-        h[i] = reinterpret_cast<const uint4*>(p.H + row * p.n)[v];
-        dy[i] = reinterpret_cast<const uint4*>(p.dY + row * p.n)[v];
-        if (p.dH) dh[i] = reinterpret_cast<const uint4*>(p.dH + row * p.n)[v];
+    h = dy = dh = make_uint4(0u, 0u, 0u, 0u);
+    rstd = 0.0f;
+    if (row < p.M) {
+      rstd = p.rstd[row];
+      if (mine) {
+        h = reinterpret_cast<const uint4*>(p.H + row * p.n)[v];
+        dy = reinterpret_cast<const uint4*>(p.dY + row * p.n)[v];
+        if (p.dH) dh = reinterpret_cast<const uint4*>(p.dH + row * p.n)[v];
       }
     }
   };
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = threadIdx.x + i * blockDim.x;
-    h[i] = dy[i] = dh[i] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dg[i][j] = g[i][j] = 0.0f;
-    if (v < nv) load_gain(p.G, p.g_f32, v, g[i]);
-  }
+  if (mine) load_gain(p.G, p.g_f32, v, g);
   int flip = 0;
-  load(blockIdx.x);
-  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, flip ^= 1) {
+  load(first + group);
+  for (int64_t r0 = first; r0 < p.M; r0 += step, flip ^= 1) {   // the same turns for every thread
+    const int64_t row = r0 + group;
     const float rs = rstd;
-    uint4 x4[VPT], d4[VPT], e4[VPT];
-    float c = 0.0f;
+    const uint4 x4 = h, d4 = dy, e4 = dh;
+    float x[8], d[8];
+    unpack8(x4, x);
+    unpack8(d4, d);
+    float2 c2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      x4[i] = h[i];
-      d4[i] = dy[i];
-      e4[i] = dh[i];
-      float x[8], d[8];
-      unpack8(x4[i], x);
-      unpack8(d4[i], d);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        c = fmaf(d[j] * g[i][j], x[j], c);
-        dg[i][j] = fmaf(d[j], x[j] * rs, dg[i][j]);
-      }
+    for (int j = 0; j < 8; j += 2) {
+      const float2 xj = make_float2(x[j], x[j + 1]), dj = make_float2(d[j], d[j + 1]);
+      c2 = fma2(mul2(dj, make_float2(g[j], g[j + 1])), xj, c2);
+      const float2 s = fma2(dj, mul2(xj, make_float2(rs, rs)), make_float2(dg[j], dg[j + 1]));
+      dg[j] = s.x;
+      dg[j + 1] = s.y;
     }
-    if (row + gridDim.x < p.M) load(row + gridDim.x);
+    load(row + step);
     // two sets of warp sums in turn: a row's are not written before every thread has
     // read those of the row before the last
-    c = warp_sum(c);
-    if (lane == 0) red[flip][warp] = c;
-    __syncthreads();
-    c = __fdiv_rn(warp_sum(lane < nw ? red[flip][lane] : 0.0f), cols) * rs * rs;
+    float c = warp_sum(c2.x + c2.y);
+    if constexpr (kCluster) {
+      if (lane < C) st_shared_cluster_f32(mapa_shared(smem_addr(&red[flip][rank * 32 + warp]), lane), c);
+      cluster_sync();
+      c = 0.0f;
+      for (int i = 0; i < C; ++i) c += lane < nw ? red[flip][i * 32 + lane] : 0.0f;
+      c = warp_sum(c);
+    } else {
+      if (lane == 0) red[flip][warp] = c;
+      __syncthreads();
+      c = warp_sum(lane < nw ? red[flip][group * nw + lane] : 0.0f);
+    }
+    c = __fdiv_rn(c, cols) * rs * rs;
+    if (mine && row < p.M) {
+      float e[8];
+      unpack8(x4, x);
+      unpack8(d4, d);
+      unpack8(e4, e);   // zeros without dH
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < nv) {
-        float x[8], d[8];
-        unpack8(x4[i], x);
-        unpack8(d4[i], d);
+      for (int j = 0; j < 8; j += 2) {
+        const float2 gd = mul2(make_float2(d[j], d[j + 1]), make_float2(g[j], g[j + 1]));
+        const float2 o = fma2(make_float2(rs, rs), fma2(make_float2(-c, -c), make_float2(x[j], x[j + 1]), gd),
+                              make_float2(e[j], e[j + 1]));
+        d[j] = o.x;
+        d[j + 1] = o.y;
+      }
+      reinterpret_cast<uint4*>(p.dR + row * p.n)[v] = pack8(d);
+      if (kDrop && p.dX) {
+        uint32_t u[8];
+        words8(p.drop, off, row * p.n + 8 * v, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = rs * fmaf(-c, x[j], d[j] * g[i][j]);
-        if (p.dH) {
-          float e[8];
-          unpack8(e4[i], e);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] += e[j];
-        }
-        reinterpret_cast<uint4*>(p.dR + row * p.n)[v] = pack8(d);
-        if (kDrop && p.dX) {
-          uint32_t u[8];
-          words8(p.drop, off, row * p.n + 8 * v, u);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] = u[j] >= p.drop.threshold ? d[j] * p.keep_scale : 0.0f;
-          reinterpret_cast<uint4*>(p.dX + row * p.n)[v] = pack8(d);
-        }
+        for (int j = 0; j < 8; ++j) d[j] = u[j] >= p.drop.threshold ? d[j] * p.keep_scale : 0.0f;
+        reinterpret_cast<uint4*>(p.dX + row * p.n)[v] = pack8(d);
       }
     }
   }
-  if (p.dG) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < nv) {
-        float4* o = reinterpret_cast<float4*>(p.parts + static_cast<int64_t>(blockIdx.x) * p.n) + 2 * v;
-        o[0] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
-        o[1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
-      }
+  if (!p.dG) return;
+  if (!kCluster && groups > 1) {
+    // the groups of this CTA, added in order by the first
+    sums[2 * threadIdx.x] = make_float4(dg[0], dg[1], dg[2], dg[3]);
+    sums[2 * threadIdx.x + 1] = make_float4(dg[4], dg[5], dg[6], dg[7]);
+    __syncthreads();
+    if (group > 0) return;
+    for (int i = 1; i < groups; ++i) {
+      const float4 a = sums[2 * (threadIdx.x + i * threads)], b = sums[2 * (threadIdx.x + i * threads) + 1];
+      dg[0] += a.x;
+      dg[1] += a.y;
+      dg[2] += a.z;
+      dg[3] += a.w;
+      dg[4] += b.x;
+      dg[5] += b.y;
+      dg[6] += b.z;
+      dg[7] += b.w;
     }
+  }
+  if (mine) {
+    float4* o = reinterpret_cast<float4*>(p.parts + static_cast<int64_t>(blockIdx.x / C) * p.n) + 2 * v;
+    o[0] = make_float4(dg[0], dg[1], dg[2], dg[3]);
+    o[1] = make_float4(dg[4], dg[5], dg[6], dg[7]);
   }
 }
 
-// dG[col] = the sum of the parts.  A CTA takes 32 columns (8 threads of 4): row lane l
-// of 32 adds the parts l, l + 32, ..., and the lanes are added in order, so the bits
-// are the same every time.
+// dG[col] = the sum of the parts.  A CTA takes 16 columns (4 threads of 4) with 64 row
+// lanes: lane l adds the parts l, l + 64, ...; the lanes of a warp and then the warps
+// are added in a fixed order, so the bits are the same every time.
 __global__ void __launch_bounds__(256) rmsnorm_dgain_kernel(const float4* parts, int nparts, int64_t n, float4* dG,
                                                             int accumulate) {
-  __shared__ float4 red[32][8];
+  __shared__ float4 red[8][4];
   grid_launch_dependents();
   grid_dependency_wait();
-  const int c = threadIdx.x & 7, l = threadIdx.x >> 3;
-  const int64_t nq = n / 4, q = static_cast<int64_t>(blockIdx.x) * 8 + c;
+  const int c = threadIdx.x & 3, l = threadIdx.x >> 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t nq = n / 4, q = static_cast<int64_t>(blockIdx.x) * 4 + c;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (q < nq) {
-#pragma unroll 8
-    for (int i = l; i < nparts; i += 32) {
+#pragma unroll 5
+    for (int i = l; i < nparts; i += 64) {
       const float4 v = __ldcg(parts + i * nq + q);
       s.x += v.x;
       s.y += v.y;
@@ -396,36 +447,50 @@ __global__ void __launch_bounds__(256) rmsnorm_dgain_kernel(const float4* parts,
       s.w += v.w;
     }
   }
-  red[l][c] = s;
-  __syncthreads();
-  if (threadIdx.x >= 8 || q >= nq) return;
-  s = accumulate ? dG[q] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const float4 v = red[i][c];
-    t.x += v.x;
-    t.y += v.y;
-    t.z += v.z;
-    t.w += v.w;
+  for (int o = 4; o < 32; o <<= 1) {
+    s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+    s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+    s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
+    s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
   }
-  dG[q] = make_float4(s.x + t.x, s.y + t.y, s.z + t.z, s.w + t.w);
+  if (lane < 4) red[warp][lane] = s;
+  __syncthreads();
+  if (threadIdx.x >= 4 || q >= nq) return;
+  s = red[0][c];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    const float4 v = red[i][c];
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  if (accumulate) {
+    const float4 v = dG[q];
+    s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+  }
+  dG[q] = s;
 }
 
-constexpr int kNormParts = 296;   // most CTAs of the gradient (two per SM)
-
-// Launch as a programmatic dependent (the kernels wait before they touch memory).
+// Launch as a programmatic dependent (the kernels wait before they touch memory), in
+// clusters of `cluster` CTAs.
 template <typename... P, typename... A>
-void launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, cudaStream_t stream, A... args) {
+void launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, unsigned cluster, cudaStream_t stream,
+                      A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   cudaLaunchKernelEx(&cfg, kernel, args...);   // a failure is the last error, read by the caller
 }
 
@@ -439,39 +504,24 @@ void fwd_plan(int64_t M, int64_t nv, int& vpt, int& threads) {
   threads = static_cast<int>(((nv + vpt - 1) / vpt + 31) / 32 * 32);
 }
 
-// Gradient: a thread keeps 16 floats of gain and its gradient a vector, so one vector
-// a thread as far as 1024 threads go; a row of more than 8192 columns spills.
-void bwd_plan(int64_t nv, int& vpt, int& threads) {
-  vpt = nv <= 1024 ? 1 : (nv <= 2048 ? 2 : (nv <= 4096 ? 4 : 8));
-  threads = static_cast<int>(((nv + vpt - 1) / vpt + 31) / 32 * 32);
-}
-
 template <int VPT>
 void run_fwd(const NormFwd& a, int threads, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(a.M);
   const int quant = a.Q ? (a.q_block ? 2 : 1) : 0;
   if (a.drop.on) {
-    if (quant == 0) launch_dependent(rmsnorm_fwd_kernel<VPT, true, 0>, grid, threads, stream, a);
-    else if (quant == 1) launch_dependent(rmsnorm_fwd_kernel<VPT, true, 1>, grid, threads, stream, a);
-    else launch_dependent(rmsnorm_fwd_kernel<VPT, true, 2>, grid, threads, stream, a);
+    if (quant == 0) launch_dependent(rmsnorm_fwd_kernel<VPT, true, 0>, grid, threads, 1, stream, a);
+    else if (quant == 1) launch_dependent(rmsnorm_fwd_kernel<VPT, true, 1>, grid, threads, 1, stream, a);
+    else launch_dependent(rmsnorm_fwd_kernel<VPT, true, 2>, grid, threads, 1, stream, a);
   } else {
-    if (quant == 0) launch_dependent(rmsnorm_fwd_kernel<VPT, false, 0>, grid, threads, stream, a);
-    else if (quant == 1) launch_dependent(rmsnorm_fwd_kernel<VPT, false, 1>, grid, threads, stream, a);
-    else launch_dependent(rmsnorm_fwd_kernel<VPT, false, 2>, grid, threads, stream, a);
+    if (quant == 0) launch_dependent(rmsnorm_fwd_kernel<VPT, false, 0>, grid, threads, 1, stream, a);
+    else if (quant == 1) launch_dependent(rmsnorm_fwd_kernel<VPT, false, 1>, grid, threads, 1, stream, a);
+    else launch_dependent(rmsnorm_fwd_kernel<VPT, false, 2>, grid, threads, 1, stream, a);
   }
 }
 
-template <int VPT>
-void run_bwd(const NormBwd& a, int grid, int threads, cudaStream_t stream) {
-  if (a.drop.on) launch_dependent(rmsnorm_bwd_kernel<VPT, true>, grid, threads, stream, a);
-  else launch_dependent(rmsnorm_bwd_kernel<VPT, false>, grid, threads, stream, a);
-}
-
-int bwd_grid(int64_t M) { return static_cast<int>(std::min<int64_t>(M, kNormParts)); }
-
 }  // namespace
 
-size_t norm_bwd_parts_bytes(int64_t M, int64_t n) { return static_cast<size_t>(bwd_grid(M)) * n * sizeof(float); }
+size_t norm_bwd_parts_bytes(int64_t M, int64_t n) { return static_cast<size_t>(bwd_plan(M, n).ctas) * n * sizeof(float); }
 
 cudaError_t launch_rmsnorm_fwd(const NormFwd& a, cudaStream_t stream) {
   int vpt, threads;
@@ -487,19 +537,20 @@ cudaError_t launch_rmsnorm_fwd(const NormFwd& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_rmsnorm_bwd(const NormBwd& a, cudaStream_t stream) {
-  int vpt, threads;
-  bwd_plan(a.n / 8, vpt, threads);
-  const int grid = bwd_grid(a.M);
+  const BwdPlan b = bwd_plan(a.M, a.n);
+  const unsigned grid = static_cast<unsigned>(b.ctas * b.cluster), threads = static_cast<unsigned>(b.threads * b.groups);
   timing_before(QLORA_KERNEL_RMSNORM_BWD, stream);
-  if (vpt == 1) run_bwd<1>(a, grid, threads, stream);
-  else if (vpt == 2) run_bwd<2>(a, grid, threads, stream);
-  else if (vpt == 4) run_bwd<4>(a, grid, threads, stream);
-  else run_bwd<8>(a, grid, threads, stream);
+  if (b.cluster > 1)
+    launch_dependent(a.drop.on ? rmsnorm_bwd_kernel<true, true> : rmsnorm_bwd_kernel<false, true>, grid, threads,
+                     static_cast<unsigned>(b.cluster), stream, a, b.threads, b.groups);
+  else
+    launch_dependent(a.drop.on ? rmsnorm_bwd_kernel<true, false> : rmsnorm_bwd_kernel<false, false>, grid, threads, 1,
+                     stream, a, b.threads, b.groups);
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && a.dG) {
-    launch_dependent(rmsnorm_dgain_kernel, static_cast<unsigned>((a.n + 31) / 32), 256, stream,
-                     reinterpret_cast<const float4*>(a.parts), grid, a.n, reinterpret_cast<float4*>(a.dG),
+    launch_dependent(rmsnorm_dgain_kernel, static_cast<unsigned>((a.n + 15) / 16), 256, 1, stream,
+                     reinterpret_cast<const float4*>(a.parts), b.ctas, a.n, reinterpret_cast<float4*>(a.dG),
                      a.accumulate ? 1 : 0);
     count_launch();
     e = cudaGetLastError();
