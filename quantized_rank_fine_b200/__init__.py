@@ -163,16 +163,17 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _empty(shape, dtype, device, stream=None):
-    """A new tensor whose memory belongs to the stream the call runs on."""
+def _empty(like, shape, dtype, stream=None):
+    """A new tensor on the device of `like`, whose memory belongs to the stream the
+    call runs on."""
     if stream is None or not isinstance(stream, torch.cuda.Stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _empty_like(t, dtype, stream=None):
-    """_empty with the shape and device of t (the shorter way through torch)."""
+    """_empty of the shape of t (the shortest way through torch)."""
     if stream is None or not isinstance(stream, torch.cuda.Stream):
         return torch.empty_like(t, dtype=dtype)
     with torch.cuda.stream(stream):
@@ -441,7 +442,8 @@ def qlora_dropout_mask(M: int, n: int, dropout: Dropout, device="cuda", stream=N
     """The mask that `dropout` stands for on an (M, n) tensor: uint8, 1 = keep.
     Passed as dropout_keep it gives the same bits as the Dropout itself."""
     if out is None:
-        out = _empty((M, n), torch.uint8, torch.device(device), stream)
+        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else _nullcontext():
+            out = torch.empty((M, n), dtype=torch.uint8, device=device)
     d = dropout.c_struct()
     _check(lib().qlora_dropout_mask(ctypes.byref(d), M, n, _ptr(out), _stream(stream)), "qlora_dropout_mask")
     return out
@@ -599,11 +601,11 @@ def qlora_rmsnorm_fwd(X: torch.Tensor, G: torch.Tensor, eps: float = 1e-5, resid
     act = codes = scales = rstd = None
     if quant_block is not None:
         act = Act8(_empty_like(X, torch.uint8, stream),
-                   _empty((M, n // quant_block if quant_block > 0 else 1), torch.float32, X.device, stream),
+                   _empty(X, (M, n // quant_block if quant_block > 0 else 1), torch.float32, stream),
                    quant_block)
         codes, scales = act.codes.data_ptr(), act.scales.data_ptr()
     if save_rstd:
-        rstd = _empty((M,), torch.float32, X.device, stream)
+        rstd = _empty(X, (M,), torch.float32, stream)
     _check(lib().qlora_rmsnorm_fwd(x, res, gain, gain_code, eps, M, n, drop, _arg(H, shape, bf16),
                                    _arg(Y, shape, bf16), codes, scales, quant_block or 0,
                                    rstd.data_ptr() if save_rstd else None, _stream(stream)), "qlora_rmsnorm_fwd")
@@ -630,7 +632,7 @@ def qlora_rmsnorm_bwd(dY: torch.Tensor, H: torch.Tensor, G: torch.Tensor, rstd: 
     if need_dG:
         dg = _arg(dG, (n,), f32)
         if dG is None:
-            dG = _empty((n,), f32, H.device, stream)
+            dG = _empty(H, (n,), f32, stream)
             dg = dG.data_ptr()
         buf = workspace.get(max(_WS_PREFIX, lib().qlora_rmsnorm_ws_bytes(M, n)), stream)
         ws, nb = buf.data_ptr(), buf.numel()
@@ -667,11 +669,11 @@ def qlora_matvec(w: NF4Weight, X, workspace: Workspace, A=None, B=None, adapter_
     r = 0 if A is None else A.shape[1]
     a, b = _arg(A, (K, r), bf16), _arg(B, (r, N), bf16)
     if Y is None:
-        Y = _empty((M, N), bf16, X.device, stream)
+        Y = _empty(X, (M, N), bf16, stream)
     if not save_V or r == 0:
         V = None
     elif V is None:
-        V = _empty((M, r), bf16, X.device, stream)
+        V = _empty(X, (M, r), bf16, stream)
     buf = workspace.get(_WS_PREFIX, stream)
     ws = w.c_struct()
     _check(lib().qlora_matvec(ctypes.byref(ws), x, scales, block, M, a, b, r, adapter_scale,

@@ -362,6 +362,16 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_bwd_kernel(const __gr
       dg[j + 1] = s.y;
     }
     load(row + step);
+    // A cluster's barrier is a long wait with one CTA an SM: the row's mask is formed
+    // before it (2048 x 16384: 108 -> 90 us).  Other CTAs fill an SM's wait at a
+    // CTA's barrier, where packing the mask into bits only costs (8192 x 4096: 69 -> 79).
+    uint32_t kept = 0;
+    if (kCluster && kDrop && p.dX && row < p.M) {
+      uint32_t u[8];
+      words8(p.drop, off, row * p.n + 8 * v, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) kept |= u[j] >= p.drop.threshold ? 1u << j : 0u;
+    }
     // two sets of warp sums in turn: a row's are not written before every thread has
     // read those of the row before the last
     float c = warp_sum(c2.x + c2.y);
@@ -393,9 +403,10 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_bwd_kernel(const __gr
       reinterpret_cast<uint4*>(p.dR + row * p.n)[v] = pack8(d);
       if (kDrop && p.dX) {
         uint32_t u[8];
-        words8(p.drop, off, row * p.n + 8 * v, u);
+        if constexpr (!kCluster) words8(p.drop, off, row * p.n + 8 * v, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = u[j] >= p.drop.threshold ? d[j] * p.keep_scale : 0.0f;
+        for (int j = 0; j < 8; ++j)
+          d[j] = (kCluster ? (kept >> j) & 1u : u[j] >= p.drop.threshold) ? d[j] * p.keep_scale : 0.0f;
         reinterpret_cast<uint4*>(p.dX + row * p.n)[v] = pack8(d);
       }
     }
