@@ -54,10 +54,14 @@ struct MvArgs {
   uint32_t* status;
 };
 
+enum : int { kXBf16 = 0, kXRow = 1, kXBlock = 2 };
+
 // TW: columns of a CTA.  MT: token tiles of 8.  RC: adapter columns held (0: no
-// adapter; 16, 64, 128, 256).  X8: x in E4M3 codes with scales, else bf16.
-template <int TW, int MT, int RC, bool X8>
+// adapter; 16, 64, 128, 256).  XM: x in bf16, or in E4M3 codes with one scale a row or
+// one per 64 columns.
+template <int TW, int MT, int RC, int XM>
 struct MvLayout {
+  static constexpr bool X8 = XM != kXBf16;
   static constexpr int kTok = MT * 8;
   static constexpr int kRows = kMvWeights / TW;                     // rows a stage
   // columns of a warp: wide where the accumulators allow it, as x is unpacked once for all of them
@@ -72,8 +76,8 @@ struct MvLayout {
   // (boxes of 16 columns, or of 64)
   static constexpr int kCodePieces = TW / 32, kScalePieces = TW / 64;
   static constexpr uint32_t kX = 8192;
-  static constexpr uint32_t kXRow = X8 ? 64 : 128;
-  static constexpr uint32_t kXBox = kTok * kXRow;
+  static constexpr uint32_t kXPitch = X8 ? 64 : 128;
+  static constexpr uint32_t kXBox = kTok * kXPitch;
   static constexpr uint32_t kScale = kX + kRows / 64 * kXBox;
   static constexpr uint32_t kA = (kScale + 4096 + 1023) / 1024 * 1024;
   static constexpr int kABox = RC < 64 ? RC : 64;                   // columns a box
@@ -83,7 +87,10 @@ struct MvLayout {
   static constexpr int kPartPitch = TW + 4;                         // floats a row of a partial tile
   static constexpr int kVPitch = kTok + 4;
   static constexpr int kWPitch = RC + 8;
-  static constexpr uint32_t kW = kKS * RC * kVPitch * 4;
+  // one adapter tile: the column groups take the row steps in turn, and each warp has a V of its own
+  static constexpr bool kTurns = RC == 16 && kNC > 1;
+  static constexpr int kVs = kTurns ? kMvWarps : kKS;
+  static constexpr uint32_t kW = kVs * RC * kVPitch * 4;
   static constexpr uint32_t kPart = kW + (RC ? 2 * kTok * kWPitch * 2 : 0);
   static constexpr uint32_t kTail = kPart + kKS * kTok * kPartPitch * 4;
   static constexpr uint32_t kRecv = (kTok * TW / 4 + kTok * RC / 4 + kMvMaxCluster) * 16;
@@ -152,11 +159,12 @@ __device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_
   lo = pack_bf16x2(v0 - bf16_lo(hi), v1 - bf16_hi(hi));
 }
 
-template <int TW, int MT, int RC, bool X8>
-__global__ void __launch_bounds__(kMvThreads, (MvLayout<TW, MT, RC, X8>::kCtas))
+template <int TW, int MT, int RC, int XM>
+__global__ void __launch_bounds__(kMvThreads, (MvLayout<TW, MT, RC, XM>::kCtas))
 matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_scales,
               const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_a, const MvArgs p) {
-  using L = MvLayout<TW, MT, RC, X8>;
+  using L = MvLayout<TW, MT, RC, XM>;
+  constexpr bool X8 = L::X8, blocked = XM == kXBlock;
   constexpr int D = L::kDepth, RT = L::kRT, TOK = L::kTok, NC = L::kNC, KS = L::kKS, G = L::kGroups;
   extern __shared__ uint8_t smem_raw[];
   // aligned by an offset, not through an integer: the compiler then knows a shared address
@@ -192,7 +200,7 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
 
   // The copies of stage i into slot s (one lane).
   auto issue = [&](int i, int s) {
-    const uint32_t bytes = 8192 + 4096 + L::kRows * RC * 2 + L::kRows / 64 * static_cast<uint32_t>(p.M) * L::kXRow;
+    const uint32_t bytes = 8192 + 4096 + L::kRows * RC * 2 + L::kRows / 64 * static_cast<uint32_t>(p.M) * L::kXPitch;
     const uint32_t dst = smem_addr(smem + s * L::kStage), bar = full0 + 8 * s;
     const int32_t k = static_cast<int32_t>(kbeg + static_cast<int64_t>(i) * L::kRows);
     mbar_arrive_expect_tx(bar, bytes);
@@ -221,8 +229,9 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
 #pragma unroll
       for (int c = 0; c < 4; ++c) vacc[a][j][c] = 0.0f;
 
-  // scales of 8-bit x: tokens g and g + 8, one per row or one per 64 rows (a warp's rows
-  // of a stage lie in one block of 64)
+  // Scales of 8-bit x.  One a row: the loop multiplies with the codes alone, exact in
+  // bf16, and the finished sums are scaled.  One per 64 rows: those of tokens g and
+  // g + 8 (a warp's rows of a stage lie in one block of 64).
   const int64_t nblk = p.K / 64;
   float xs[MT];
   auto load_xs = [&](int i) {
@@ -230,10 +239,10 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
     for (int a = 0; a < MT; ++a) {
       const int64_t m = a * 8 + g < p.M ? a * 8 + g : 0;   // a column past M is never stored
       const int64_t blk = kbeg / 64 + L::kRows / 64 * i + ks * L::kSteps / 4;
-      xs[a] = __ldg(p.x_scales + (p.x_block ? m * nblk + (blk < nblk ? blk : 0) : m));
+      xs[a] = __ldg(p.x_scales + m * nblk + (blk < nblk ? blk : 0));
     }
   };
-  if (X8) load_xs(0);
+  if constexpr (blocked) load_xs(0);
 
   // The lane's rows of a 16-row step are 4t + (i ^ (t >> 1)), i = 0 .. 3: with the swizzles
   // above, the four lanes' scales of one i then lie on different banks, and so do the
@@ -280,8 +289,8 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
     const uint32_t base = base0 + s * L::kStage;
     float xs_now[MT];
 #pragma unroll
-    for (int a = 0; a < MT; ++a) xs_now[a] = xs[a];
-    if (X8 && p.x_block && i + 1 < nst) load_xs(i + 1);
+    for (int a = 0; a < MT; ++a) xs_now[a] = blocked ? xs[a] : 1.0f;
+    if (blocked && i + 1 < nst) load_xs(i + 1);
 
 #pragma unroll
     for (int h = 0; h < L::kSteps; ++h) {   // 16-row steps
@@ -298,10 +307,14 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
           const float2 f0 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<uint16_t>(c), __NV_E4M3)));
           const float2 f1 =
               __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<uint16_t>(c >> 16), __NV_E4M3)));
-          x[a][0] = f0.x * xs_now[a];
-          x[a][1] = f0.y * xs_now[a];
-          x[a][2] = f1.x * xs_now[a];
-          x[a][3] = f1.y * xs_now[a];
+          x[a][0] = f0.x;
+          x[a][1] = f0.y;
+          x[a][2] = f1.x;
+          x[a][3] = f1.y;
+          if constexpr (blocked) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[a][k] *= xs_now[a];
+          }
         } else {
           const uint2 c = *reinterpret_cast<const uint2*>(
               at + L::kX + (kstep / 4) * L::kXBox + piece<8>(m, 2 * (kstep & 3) + (t >> 1)) + 8 * (t & 1));
@@ -315,13 +328,17 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
       }
 
       if constexpr (RC > 0) {
-        if (16 * cg < p.r) {
-          uint32_t xh[MT][2], xl[MT][2];   // x for the adapter: exact, or (8-bit x) a sum of two bf16 terms
+        if (L::kTurns ? (i * L::kSteps + h) % NC == cg : 16 * cg < p.r) {
+          uint32_t xh[MT][2], xl[MT][2];   // x for the adapter: exact, or (with block scales) a sum of two bf16 terms
 #pragma unroll
           for (int a = 0; a < MT; ++a) {
             if constexpr (X8) {
-              split2(x[a][0], x[a][1], xh[a][0], xl[a][0]);
-              split2(x[a][2], x[a][3], xh[a][1], xl[a][1]);
+              xh[a][0] = pack_bf16x2(x[a][0], x[a][1]);
+              xh[a][1] = pack_bf16x2(x[a][2], x[a][3]);
+              if constexpr (blocked) {
+                split2(x[a][0], x[a][1], xh[a][0], xl[a][0]);
+                split2(x[a][2], x[a][3], xh[a][1], xl[a][1]);
+              }
             } else {
               xh[a][0] = xb[a][0];
               xh[a][1] = xb[a][1];
@@ -329,7 +346,7 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
           }
 #pragma unroll
           for (int j = 0; j < RT; ++j) {
-            if (16 * (NC * j + cg) < p.r) {   // tile NC j + cg of 16 adapter columns
+            if (L::kTurns || 16 * (NC * j + cg) < p.r) {   // tile NC j + cg of 16 adapter columns
               uint32_t a0, a1, a2, a3;
               asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                            : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
@@ -337,7 +354,7 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
 #pragma unroll
               for (int a = 0; a < MT; ++a) {
                 mv_mma(vacc[a][j], a0, a1, a2, a3, xh[a][0], xh[a][1]);
-                if constexpr (X8) mv_mma(vacc[a][j], a0, a1, a2, a3, xl[a][0], xl[a][1]);
+                if constexpr (blocked) mv_mma(vacc[a][j], a0, a1, a2, a3, xl[a][0], xl[a][1]);
               }
             }
           }
@@ -396,7 +413,7 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
   }
 
   // ------------------------------------------------------------ V of this CTA's rows, times B
-  float* Vs = reinterpret_cast<float*>(smem);                                // [KS][ranks][kVPitch]
+  float* Vs = reinterpret_cast<float*>(smem);                                // [kVs][ranks][kVPitch]
   uint16_t* W = reinterpret_cast<uint16_t*>(smem + L::kW);                   // [2 terms][tok][kWPitch]
   float* part = reinterpret_cast<float*>(smem + L::kPart);                   // [KS][tok][L::kPartPitch]
   if constexpr (RC > 0) {
@@ -418,11 +435,11 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
     __syncthreads();   // every ring is free
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
-      const int tr = 16 * (NC * j + cg);
+      const int tr = L::kTurns ? 0 : 16 * (NC * j + cg);
       if (tr < p.r) {
 #pragma unroll
         for (int a = 0; a < MT; ++a) {
-          float* d = Vs + (ks * RC + tr + g) * L::kVPitch + a * 8 + 2 * t;
+          float* d = Vs + ((L::kTurns ? warp : ks) * RC + tr + g) * L::kVPitch + a * 8 + 2 * t;
           *reinterpret_cast<float2*>(d) = make_float2(vacc[a][j][0] * p.scale, vacc[a][j][1] * p.scale);
           *reinterpret_cast<float2*>(d + 8 * L::kVPitch) = make_float2(vacc[a][j][2] * p.scale, vacc[a][j][3] * p.scale);
         }
@@ -435,7 +452,7 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
       float v = 0.0f;
       if (j < p.r)
 #pragma unroll
-        for (int k = 0; k < KS; ++k) v += Vs[(k * RC + j) * L::kVPitch + m];
+        for (int k = 0; k < L::kVs; ++k) v += Vs[(k * RC + j) * L::kVPitch + m];
       uint32_t hi, lo;
       split2(v, 0.0f, hi, lo);
       W[m * L::kWPitch + j] = static_cast<uint16_t>(hi);
@@ -506,13 +523,20 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
     } else {
       const int e = 4 * (q - gy), m = e / p.r;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
+      for (int k = 0; k < L::kVs; ++k) {
         const float* src = Vs + (k * RC + e % p.r) * L::kVPitch + m;
         v.x += src[0];
         v.y += src[L::kVPitch];
         v.z += src[2 * L::kVPitch];
         v.w += src[3 * L::kVPitch];
       }
+    }
+    if constexpr (XM == kXRow) {   // the scales of the rows
+      const float f = __ldg(p.x_scales + (q < gy ? q / (TW / 4) : 4 * (q - gy) / p.r));
+      v.x *= f;
+      v.y *= f;
+      v.z *= f;
+      v.w *= f;
     }
     const int o = q / cap, to = q - o * cap;
     st_shared_cluster_v4(mapa_shared(recv_addr + static_cast<uint32_t>((rank * cap + to) * 16), o), v);
@@ -546,7 +570,7 @@ struct MvFit {
   int max_active[kMvMaxCluster + 1] = {};
 };
 
-template <int TW, int MT, int RC, bool X8>
+template <int TW, int MT, int RC, int XM>
 const MvFit& mv_fit() {
   static std::mutex mu;
   static MvFit fits[64];
@@ -556,8 +580,8 @@ const MvFit& mv_fit() {
   std::lock_guard<std::mutex> lock(mu);
   MvFit& f = fits[dev];
   if (f.done) return f;
-  auto fn = matvec_kernel<TW, MT, RC, X8>;
-  constexpr uint32_t bytes = MvLayout<TW, MT, RC, X8>::kSmem;
+  auto fn = matvec_kernel<TW, MT, RC, XM>;
+  constexpr uint32_t bytes = MvLayout<TW, MT, RC, XM>::kSmem;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess ||
       cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
     cudaGetLastError();
@@ -640,13 +664,13 @@ struct MvInputs {
   const uint16_t* A;
 };
 
-template <int TW, int MT, int RC, bool X8>
+template <int TW, int MT, int RC, int XM>
 cudaError_t run_matvec(MvArgs a, int S, const MvInputs& in, cudaStream_t stream) {
-  using L = MvLayout<TW, MT, RC, X8>;
+  using L = MvLayout<TW, MT, RC, XM>;
   CUtensorMap tc, ts, tx, ta;
   if (!mv_map(&tc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, in.codes, a.K, a.N / 2, TW / 2, L::kRows) ||
       !mv_map(&ts, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, in.scales, a.K, a.N / 16, TW / 16, L::kRows) ||
-      !(X8 ? mv_map(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, in.x, a.M, a.K, 64, a.M)
+      !(L::X8 ? mv_map(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, in.x, a.M, a.K, 64, a.M)
            : mv_map(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, in.x, a.M, a.K, 64, a.M)) ||
       (RC > 0 && !mv_map(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, in.A, a.K, a.r, L::kABox, L::kRows)))
     return cudaErrorInvalidValue;
@@ -666,7 +690,7 @@ cudaError_t run_matvec(MvArgs a, int S, const MvInputs& in, cudaStream_t stream)
   cfg.attrs = at;
   cfg.numAttrs = 2;
   timing_before(QLORA_KERNEL_MATVEC, stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, matvec_kernel<TW, MT, RC, X8>, tc, ts, tx, ta, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, matvec_kernel<TW, MT, RC, XM>, tc, ts, tx, ta, a);
   timing_after(QLORA_KERNEL_MATVEC, stream);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -675,24 +699,25 @@ cudaError_t run_matvec(MvArgs a, int S, const MvInputs& in, cudaStream_t stream)
 // The tile width with the lower cost: 128 columns make twice the tiles of half the
 // clusters, which fill the device better where N gives few tiles; 256 read x and A half
 // as often.
-template <int MT, int RC, bool X8>
+template <int MT, int RC, int XM>
 cudaError_t run_by_width(MvArgs a, const MvInputs& in, cudaStream_t stream) {
   int S1 = 0, S2 = 0;
   int64_t k1 = 0, k2 = 0;
-  const int64_t c1 = mv_plan(a.K, a.N, 128, mv_fit<128, MT, RC, X8>(), S1, k1);
-  const int64_t c2 = mv_plan(a.K, a.N, 256, mv_fit<256, MT, RC, X8>(), S2, k2);
+  const int64_t c1 = mv_plan(a.K, a.N, 128, mv_fit<128, MT, RC, XM>(), S1, k1);
+  const int64_t c2 = mv_plan(a.K, a.N, 256, mv_fit<256, MT, RC, XM>(), S2, k2);
   if (c1 < 0 && c2 < 0) return cudaErrorInvalidValue;
   if (c2 < 0 || (c1 >= 0 && c1 < c2)) {
     a.Kc = k1;
-    return run_matvec<128, MT, RC, X8>(a, S1, in, stream);
+    return run_matvec<128, MT, RC, XM>(a, S1, in, stream);
   }
   a.Kc = k2;
-  return run_matvec<256, MT, RC, X8>(a, S2, in, stream);
+  return run_matvec<256, MT, RC, XM>(a, S2, in, stream);
 }
 
 template <int MT, int RC>
 cudaError_t run_by_x(const MvArgs& a, const MvInputs& in, cudaStream_t stream) {
-  return a.x_scales ? run_by_width<MT, RC, true>(a, in, stream) : run_by_width<MT, RC, false>(a, in, stream);
+  if (!a.x_scales) return run_by_width<MT, RC, kXBf16>(a, in, stream);
+  return a.x_block ? run_by_width<MT, RC, kXBlock>(a, in, stream) : run_by_width<MT, RC, kXRow>(a, in, stream);
 }
 
 template <int MT>
