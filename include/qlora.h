@@ -468,8 +468,7 @@ QLORA_API qlora_status qlora_loftq_split(const float* U, int64_t ldu, const floa
  *   Q        [device] out: y in 8 bits, uint8 (M, n) E4M3 codes, or NULL.  Per block
  *            of q_block columns (64, or 0 for the whole row): a = max |y|,
  *            s = fl32(a / 448) (0 where that is below 2^-126), code =
- *            E4M3(fl32(y fl32(1 / s))) round to nearest even (0 where s = 0), so
- *            y ~ code s.  y is not rounded to bf16 in between.  A block that holds a
+ *            E4M3(fl32(y / s)) round to nearest even (0 where s = 0), so y ~ code s.  y is not rounded to bf16 in between.  A block that holds a
  *            NaN or an infinity gets codes and a scale whose products are NaN.
  *   q_scales [device] out: fp32 (M, n / 64), or (M) with q_block = 0.  With Q only.
  *   rstd     [device] out: fp32 (M), for the backward, or NULL.

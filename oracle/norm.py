@@ -10,7 +10,7 @@ stands between two of them:
   rstd = 1 / sqrt(mean h^2 + eps).  h is rounded to bf16 before the norm, as it is
   what the next layer's residual stream holds.
 * 8-bit y: per block a = max |y|, scale = fl32(a / 448) (0 below 2^-126), code =
-  E4M3(fl32(y fl32(1 / scale))).
+  E4M3(fl32(y / scale)).
 * dh = rstd (g dy - h mean(g dy h) rstd^2) + dH; dx = keep s dh; dg = sum dy h rstd.
 * The words of Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random
   numbers: as easy as 1, 2, 3", 2011): element e takes word e mod 4 of the counter
@@ -97,7 +97,7 @@ def quantize_e4m3(y, block: int):
     b = y.reshape(M, -1, block or n)
     s = fl32(np.abs(b).max(axis=2) / 448.0).astype(np.float64)
     s = np.where(s < 2.0 ** -126, 0.0, s)
-    inv = fl32(1.0 / np.where(s > 0, s, 1.0)).astype(np.float64)
-    v = np.where(s[:, :, None] > 0, fl32(b * inv[:, :, None]).astype(np.float64), 0.0).reshape(-1)
+    safe = np.where(s > 0, s, 1.0)
+    v = np.where(s[:, :, None] > 0, fl32(b / safe[:, :, None]).astype(np.float64), 0.0).reshape(-1)
     sign = np.where(v < 0, -1.0, 1.0)
     return (sign * e4m3_decode(e4m3_encode(np.abs(v).astype(np.float32)))).reshape(M, n), s

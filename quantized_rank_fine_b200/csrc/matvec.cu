@@ -244,6 +244,25 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
   };
   if constexpr (blocked) load_xs(0);
 
+  // B of 16 adapter rows and this warp's groups of columns (kOwn ks, ... of its columns).
+  // With one token tile the first are loaded here, so that nothing waits for them after
+  // the loop (4096 x 4096, 1 token: 7.8 -> 7.4 us); two token tiles have no registers
+  // left for that (they spilled: 19.2 -> 23.3 us at 4096 x 11008 with block scales).
+  constexpr int OWN = L::kOwn;
+  const int64_t bcol = col0 + 16 * OWN * ks + 2 * g;
+  uint32_t bw[OWN][4] = {};
+  auto load_b = [&](int j0) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = j0 + 2 * t + (u & 1) + 8 * (u >> 1);
+      const bool in = row < p.r && bcol < p.N;   // N is a multiple of 64: a warp's groups lie inside or outside
+#pragma unroll
+      for (int o = 0; o < OWN; ++o)
+        bw[o][u] = in ? __ldg(reinterpret_cast<const uint32_t*>(p.B + row * p.N + bcol + 16 * o)) : 0u;
+    }
+  };
+  if constexpr (RC > 0 && MT == 1) load_b(0);
+
   // The lane's rows of a 16-row step are 4t + (i ^ (t >> 1)), i = 0 .. 3: with the swizzles
   // above, the four lanes' scales of one i then lie on different banks, and so do the
   // eight code rows of each phase of the transposing load.
@@ -417,21 +436,7 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
   uint16_t* W = reinterpret_cast<uint16_t*>(smem + L::kW);                   // [2 terms][tok][kWPitch]
   float* part = reinterpret_cast<float*>(smem + L::kPart);                   // [KS][tok][L::kPartPitch]
   if constexpr (RC > 0) {
-    // B of the first 16 adapter rows and this warp's groups of columns (kOwn ks, ... of its columns)
-    constexpr int OWN = L::kOwn;
-    const int64_t bcol = col0 + 16 * OWN * ks + 2 * g;
-    uint32_t bw[OWN][4];
-    auto load_b = [&](int j0) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int row = j0 + 2 * t + (u & 1) + 8 * (u >> 1);
-        const bool in = row < p.r && bcol < p.N;   // N is a multiple of 64: a warp's groups lie inside or outside
-#pragma unroll
-        for (int o = 0; o < OWN; ++o)
-          bw[o][u] = in ? __ldg(reinterpret_cast<const uint32_t*>(p.B + row * p.N + bcol + 16 * o)) : 0u;
-      }
-    };
-    load_b(0);
+    if constexpr (MT == 2) load_b(0);
     __syncthreads();   // every ring is free
 #pragma unroll
     for (int j = 0; j < RT; ++j) {

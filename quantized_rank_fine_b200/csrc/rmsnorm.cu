@@ -3,7 +3,7 @@
 //
 //   h = bf16(res + keep x / (1 - p)),  rstd = 1 / sqrt(mean(h^2) + eps),  y = h rstd g
 //   out: h (bf16), bf16(y), and y in 8 bits: per row or per 64 columns
-//        s = fl32(max|y| / 448), code = E4M3(fl32(y fl32(1 / s)))
+//        s = fl32(max|y| / 448), code = E4M3(fl32(y / s))
 //   gh = g dy,  c = mean(gh h) rstd^2,  dh = rstd (gh - h c) + dH
 //   out: dR = bf16(dh), dX = bf16(keep dh / (1 - p)), dG = sum over rows of dy h rstd
 //
@@ -150,12 +150,23 @@ __device__ __forceinline__ float block_scale(uint32_t top) {
   return s < 0x1p-126f ? 0.0f : s;
 }
 
-// E4M3(fl32(y fl32(1 / s))) of eight values, 0 where s = 0.
+// E4M3(fl32(y / s)) of eight values, 0 where s = 0.  The quotients by Markstein's
+// theorem (IBM Journal of Research and Development 34, 1990): with the reciprocal r
+// of s, the product q = y r and the rest y - q s, each rounded once, q + (y - q s) r
+// is the correctly rounded quotient, as long as the rest does not underflow (|y|
+// above about 2^-100).
 __device__ __forceinline__ uint2 e4m3_codes(const float (&y)[8], float s) {
   if (s == 0.0f) return make_uint2(0u, 0u);
   const float inv = __frcp_rn(s);
-  return make_uint2(e4m3_pair(y[0] * inv, y[1] * inv) | (e4m3_pair(y[2] * inv, y[3] * inv) << 16),
-                    e4m3_pair(y[4] * inv, y[5] * inv) | (e4m3_pair(y[6] * inv, y[7] * inv) << 16));
+  const float2 r2 = make_float2(inv, inv), s2 = make_float2(-s, -s);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = make_float2(y[2 * i], y[2 * i + 1]), q0 = mul2(v, r2);
+    const float2 q = fma2(fma2(q0, s2, v), r2, q0);
+    w[i] = e4m3_pair(q.x, q.y);
+  }
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
 // bf16(a + b) of pairs, one rounding.

@@ -100,6 +100,22 @@ def test_codes_are_the_oracles_where_y_is_exact():
         assert np.array_equal(_np(o.act.codes.view(torch.float8_e4m3fn).float()), v)
 
 
+def test_codes_of_random_quotients():
+    """y made exact again (rstd = 1/2 on rows of +-1, gains of 24 bits): a million
+    quotients y / s over many scales, every code as from the IEEE quotient."""
+    M, n = 64, 16384
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = (torch.randint(0, 2, (M, n), generator=gen, device="cuda") * 2 - 1).to(BF)
+    for lo in (-20, -60):
+        g = torch.randn(n, generator=gen, device="cuda") * torch.exp2(torch.randint(lo, 8, (n,), generator=gen, device="cuda").float())
+        o = q.qlora_rmsnorm_fwd(x, g, 3.0, want_y=False, quant_block=64)
+        v, s = norm.quantize_e4m3(_np(x[:1]) * 0.5 * _np(g), 64)
+        got = _np(o.act.codes.view(torch.float8_e4m3fn).float())
+        assert np.array_equal(_np(o.act.scales), np.repeat(s, M, axis=0))
+        sign = _np(x) * _np(x[:1])
+        assert np.array_equal(got, sign * v)
+
+
 def test_zero_rows_and_nonfinite_values():
     n = 256
     d = _inputs(4, n)
