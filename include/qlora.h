@@ -463,7 +463,8 @@ QLORA_API qlora_status qlora_loftq_split(const float* U, int64_t ldu, const floa
  *   eps      > 0 and finite, else QLORA_ERR_INVALID_ARG.
  *   drop     [host] dropout of X (mask over (M, n)), or NULL.  A dropped X adds
  *            nothing, whatever it holds.
- *   H        [device] out: bf16 (M, n), or NULL where it is not wanted.
+ *   H        [device] out: bf16 (M, n), or NULL where it is not wanted.  It may be
+ *            R itself: every element is read before it is written.
  *   Y        [device] out: bf16(y) (M, n), or NULL.
  *   Q        [device] out: y in 8 bits, uint8 (M, n) E4M3 codes, or NULL.  Per block
  *            of q_block columns (64, or 0 for the whole row): a = max |y|,
@@ -489,6 +490,7 @@ QLORA_API qlora_status qlora_rmsnorm_fwd(const uint16_t* X, const uint16_t* R, c
  *         gradient), or NULL.
  *   drop  [host] the forward's, or NULL.
  *   dR    [device] out: bf16 (M, n), the gradient of R, and of X without dropout.
+ *         It may be dH or dY itself: every element is read before it is written.
  *   dX    [device] out: bf16 (M, n), the gradient of X under dropout, or NULL.
  *         QLORA_ERR_INVALID_ARG if given without dropout (p = 0 is none).
  *   dG    [device] out: fp32 (n), or NULL where the gain is frozen.

@@ -271,14 +271,18 @@ def qlora_workspace_bytes(op: int, M: int, n_in: int, n_out: int, r: int) -> int
 
 class Workspace:
     """Caller-owned scratch of the forward/backward calls (a device uint8 tensor),
-    grown on demand and initialised once through qlora_ws_init."""
+    grown on demand and initialised once through qlora_ws_init.  A buffer that was
+    outgrown is kept: a captured graph or a call in flight may still write to it."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = None
+        self.outgrown = []
 
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
         if self.buf is None or self.buf.numel() < nbytes:
+            if self.buf is not None:
+                self.outgrown.append(self.buf)
             self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             _check(lib().qlora_ws_init(_ptr(self.buf), self.buf.numel(), _stream(stream)), "qlora_ws_init")
         return self.buf
@@ -426,8 +430,11 @@ class Dropout:
 
 
 def _drop(dropout):
-    """The C argument of an optional Dropout (None without one, or with p = 0)."""
-    return None if dropout is None or dropout.p == 0.0 else ctypes.byref(dropout.c_struct())
+    """The C argument of an optional Dropout (None without one, or where p is 0 in fp32)."""
+    if dropout is None:
+        return None
+    s = dropout.c_struct()
+    return None if s.p == 0.0 else ctypes.byref(s)
 
 
 def _opts(adapter_scale: float, accumulate: bool = False, dropout_keep=None, dropout_p: float = 0.0, dropout=None):
@@ -588,7 +595,8 @@ def qlora_rmsnorm_fwd(X: torch.Tensor, G: torch.Tensor, eps: float = 1e-5, resid
     """h = residual + dropout(X), y = h rstd G for bf16 (M, n) rows and a gain G in
     bf16 or fp32.  The result holds H (only with a residual or dropout: else h is X
     itself), Y = bf16(y) unless want_y is False, y in 8 bits with quant_block 0 (one
-    scale a row) or 64 (one per 64 columns), and rstd for the backward."""
+    scale a row) or 64 (one per 64 columns), and rstd for the backward.  H may be the
+    residual itself (updated in place)."""
     shape, bf16 = X.shape, torch.bfloat16
     M, n = shape
     x, res = _arg(X, shape, bf16), _arg(residual, shape, bf16)
@@ -618,7 +626,8 @@ def qlora_rmsnorm_bwd(dY: torch.Tensor, H: torch.Tensor, G: torch.Tensor, rstd: 
     """Returns (dX, dR, dG): the gradients of the branch X, of the residual, and of
     the gain (fp32, None without need_dG).  H is the forward's h (its X where it had
     neither residual nor dropout), dH the gradient that reaches h past the norm.
-    Without dropout dX is dR.  With accumulate dG (given) receives the sum."""
+    Without dropout dX is dR.  With accumulate dG (given) receives the sum.  dR may be
+    dH or dY itself."""
     if accumulate and dG is None:
         raise ValueError("accumulate needs the dG to add into")
     shape, bf16, f32 = H.shape, torch.bfloat16, torch.float32
