@@ -478,7 +478,7 @@ def run_step(layers, ws):
         q.qlora_linear_bwd(w, t["X"], o["V"], t["dY"], t["A"], t["B"], ws, dX=o["dX"], dA=o["dA"], dB=o["dB"])
 
 
-ROW_NAMES = ("quantize", "dequantize", "merge", "gemv", "train_step", "int16", "mlp_m8192", "dense")
+ROW_NAMES = ("quantize", "dequantize", "merge", "gemv", "train_step", "int16", "mlp_m8192", "block", "dense")
 
 
 def time_rows(wl, pk, which="all"):
@@ -506,6 +506,11 @@ def time_rows(wl, pk, which="all"):
             rows["int16"] = time_int16_rows(wl, pk)
         except Exception as e:   # a secondary row never takes the headline down
             rows["int16"] = {"error": f"{type(e).__name__}: {e}"}
+    if "block" in want:
+        try:
+            rows["block"] = time_block_rows(pk)
+        except Exception as e:   # a secondary row never takes the headline down
+            rows["block"] = {"error": f"{type(e).__name__}: {e}"}
     if "dense" in want:
         try:
             rows["dense_context"] = time_dense_context(pk)
@@ -679,6 +684,86 @@ def time_int16_rows(wl, pk):
         raise RuntimeError("a kernel wait timed out in the INT rows")
     del ints, wts_int, wts_nf4
     torch.cuda.synchronize()
+    return out
+
+
+def graph_per_call(fn, iters):
+    """Device time (ms) per call of fn(0 .. iters - 1) captured in one CUDA graph,
+    median of five replays."""
+    import torch
+    for i in range(3):
+        fn(i)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            for i in range(iters):
+                fn(i)
+    torch.cuda.current_stream().wait_stream(side)
+    graph.replay()
+    torch.cuda.synchronize()
+    times = []
+    for _ in range(5):
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        graph.replay()
+        e1.record()
+        torch.cuda.synchronize()
+        times.append(e0.elapsed_time(e1) / iters)
+    del graph
+    return statistics.median(times)
+
+
+def time_block_rows(pk):
+    """What stands around the layer: the residual addition with RMS norm and its
+    gradient at 2048 and 8192 tokens of 4096 (the larger under dropout), and the
+    integer matrix-vector product (r = 16) at 1, 4 and 16 tokens.  Device time per
+    call of a CUDA graph of back-to-back calls over input sets larger than L2.
+    Algorithmic bytes: every input read once, every output written once."""
+    import torch
+    import quantized_rank_fine_b200 as q
+    import synth
+    bf16 = torch.bfloat16
+    out = {}
+    ws = q.Workspace()
+    n = 4096
+    g = synth.normal("blockG", (n,), 1.0, device="cuda")
+    for M, p in ((2048, 0.0), (8192, 0.1)):
+        e = M * n
+        reps = max(2, math.ceil(3 * L2_BYTES / (8 * e)))
+        sets = [[synth.normal(f"block{k}{i}", (M, n), 1.0, bf16, "cuda") for k in "xrdH"] +
+                [torch.empty((M, n), dtype=bf16, device="cuda") for _ in range(2)] for i in range(reps)]
+        drop = q.Dropout(p, 1, 2) if p else None
+        dX = torch.empty((M, n), dtype=bf16, device="cuda") if p else None
+        dG = torch.empty(n, device="cuda")
+        rstd = q.qlora_rmsnorm_fwd(sets[0][1], g, save_rstd=True).rstd
+        t = graph_per_call(lambda i: q.qlora_rmsnorm_fwd(sets[i % reps][0], g, residual=sets[i % reps][1], dropout=drop,
+                                                         H=sets[i % reps][4], Y=sets[i % reps][5]), 20)
+        out[f"norm_fwd_m{M}_p{p}"] = {"ms": t, **hbm_fracs(8 * e, t, pk)}
+        t = graph_per_call(lambda i: q.qlora_rmsnorm_bwd(sets[i % reps][2], sets[i % reps][1], g, rstd, ws,
+                                                         dH=sets[i % reps][3], dropout=drop, dR=sets[i % reps][4],
+                                                         dX=dX, dG=dG), 20)
+        out[f"norm_bwd_m{M}_p{p}"] = {"ms": t, **hbm_fracs((10 if p else 8) * e, t, pk)}
+        del sets
+    r = 16
+    for n_in, n_out in ((4096, 4096), (4096, 11008)):
+        wbytes = n_in * n_out * 0.75
+        reps = max(3, math.ceil(3 * L2_BYTES / wbytes))
+        wts = [q.int_weight(*q.qlora_quantize_int(synth.normal(f"mvW{i}", (n_in, n_out), 0.02, device="cuda"), 4), n_in,
+                            n_out) for i in range(reps)]
+        A = synth.normal("mvA", (n_in, r), 1 / math.sqrt(n_in), bf16, "cuda")
+        B = synth.normal("mvB", (r, n_out), 0.01, bf16, "cuda")
+        for M in (1, 4, 16):
+            X = synth.normal(f"mvX{M}", (M, n_in), 1.0, bf16, "cuda")
+            Y = torch.empty((M, n_out), dtype=bf16, device="cuda")
+            t = graph_per_call(lambda i: q.qlora_matvec(wts[i % reps], X, ws, A, B, Y=Y), 60)
+            b = wbytes + 2 * r * (n_in + n_out) + 2 * M * (n_in + n_out)
+            out[f"matvec_{n_in}x{n_out}_m{M}"] = {"ms": t, **hbm_fracs(b, t, pk)}
+        del wts
+    if ws.status() != 0:
+        raise RuntimeError("a kernel wait timed out in the block rows")
     return out
 
 
