@@ -475,9 +475,9 @@ def qlora_linear_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Te
     `dropout` the mask comes from the generator and is not stored."""
     M, r = X.shape[0], A.shape[1]
     if Y is None:
-        Y = torch.empty((M, w.n_out), dtype=torch.bfloat16, device=X.device)
+        Y = X.new_empty((M, w.n_out), dtype=torch.bfloat16)
     if save_V and V is None:
-        V = torch.empty((M, r), dtype=torch.bfloat16, device=X.device)
+        V = X.new_empty((M, r), dtype=torch.bfloat16)
     nb = qlora_workspace_bytes(QLORA_OP_FWD, M, w.n_in, w.n_out, r)
     buf = workspace.get(nb, stream)
     ws = w.c_struct()
@@ -599,13 +599,15 @@ def qlora_rmsnorm_fwd(X: torch.Tensor, G: torch.Tensor, eps: float = 1e-5, resid
     residual itself (updated in place)."""
     shape, bf16 = X.shape, torch.bfloat16
     M, n = shape
-    x, res = _arg(X, shape, bf16), _arg(residual, shape, bf16)
+    x, res, h, y = _arg(X, shape, bf16), _arg(residual, shape, bf16), _arg(H, shape, bf16), _arg(Y, shape, bf16)
     gain, gain_code = _gain(G, n)
     drop = _drop(dropout)
     if H is None and (residual is not None or drop is not None):
         H = _empty_like(X, bf16, stream)
+        h = H.data_ptr()
     if Y is None and want_y:
         Y = _empty_like(X, bf16, stream)
+        y = Y.data_ptr()
     act = codes = scales = rstd = None
     if quant_block is not None:
         act = Act8(_empty_like(X, torch.uint8, stream),
@@ -614,8 +616,7 @@ def qlora_rmsnorm_fwd(X: torch.Tensor, G: torch.Tensor, eps: float = 1e-5, resid
         codes, scales = act.codes.data_ptr(), act.scales.data_ptr()
     if save_rstd:
         rstd = _empty(X, (M,), torch.float32, stream)
-    _check(lib().qlora_rmsnorm_fwd(x, res, gain, gain_code, eps, M, n, drop, _arg(H, shape, bf16),
-                                   _arg(Y, shape, bf16), codes, scales, quant_block or 0,
+    _check(lib().qlora_rmsnorm_fwd(x, res, gain, gain_code, eps, M, n, drop, h, y, codes, scales, quant_block or 0,
                                    rstd.data_ptr() if save_rstd else None, _stream(stream)), "qlora_rmsnorm_fwd")
     return RMSNormOut(H, Y, act, rstd)
 
@@ -633,6 +634,7 @@ def qlora_rmsnorm_bwd(dY: torch.Tensor, H: torch.Tensor, G: torch.Tensor, rstd: 
     shape, bf16, f32 = H.shape, torch.bfloat16, torch.float32
     M, n = shape
     h, dy, dh = _arg(H, shape, bf16), _arg(dY, shape, bf16), _arg(dH, shape, bf16)
+    dr, dx = _arg(dR, shape, bf16), _arg(dX, shape, bf16)
     gain, gain_code = _gain(G, n)
     rs = _arg(rstd, (M,), f32)
     drop = _drop(dropout)
@@ -647,13 +649,15 @@ def qlora_rmsnorm_bwd(dY: torch.Tensor, H: torch.Tensor, G: torch.Tensor, rstd: 
         ws, nb = buf.data_ptr(), buf.numel()
     if dR is None:
         dR = _empty_like(H, bf16, stream)
+        dr = dR.data_ptr()
     if drop is None:
-        dX = None
+        dX = dx = None
     elif dX is None:
         dX = _empty_like(H, bf16, stream)
-    _check(lib().qlora_rmsnorm_bwd(dy, h, gain, gain_code, rs, dh, M, n, drop, _arg(dR, shape, bf16),
-                                   _arg(dX, shape, bf16), dg, QLORA_ACCUMULATE_GRADS if accumulate else 0, ws, nb,
-                                   _stream(stream)), "qlora_rmsnorm_bwd")
+        dx = dX.data_ptr()
+    _check(lib().qlora_rmsnorm_bwd(dy, h, gain, gain_code, rs, dh, M, n, drop, dr, dx, dg,
+                                   QLORA_ACCUMULATE_GRADS if accumulate else 0, ws, nb, _stream(stream)),
+           "qlora_rmsnorm_bwd")
     return (dR if drop is None else dX), dR, (dG if need_dG else None)
 
 
@@ -676,18 +680,21 @@ def qlora_matvec(w: NF4Weight, X, workspace: Workspace, A=None, B=None, adapter_
     if K != w.n_in:
         raise ValueError(f"X has {K} columns, the weight {w.n_in} rows")
     r = 0 if A is None else A.shape[1]
-    a, b = _arg(A, (K, r), bf16), _arg(B, (r, N), bf16)
+    a, b, y, v = _arg(A, (K, r), bf16), _arg(B, (r, N), bf16), _arg(Y, (M, N), bf16), None
     if Y is None:
         Y = _empty(X, (M, N), bf16, stream)
+        y = Y.data_ptr()
     if not save_V or r == 0:
         V = None
     elif V is None:
         V = _empty(X, (M, r), bf16, stream)
+        v = V.data_ptr()
+    else:
+        v = _arg(V, (M, r), bf16)
     buf = workspace.get(_WS_PREFIX, stream)
     ws = w.c_struct()
-    _check(lib().qlora_matvec(ctypes.byref(ws), x, scales, block, M, a, b, r, adapter_scale,
-                              _arg(Y, (M, N), bf16), _arg(V, (M, r), bf16), buf.data_ptr(),
-                              buf.numel(), _stream(stream)), "qlora_matvec")
+    _check(lib().qlora_matvec(ctypes.byref(ws), x, scales, block, M, a, b, r, adapter_scale, y, v,
+                              buf.data_ptr(), buf.numel(), _stream(stream)), "qlora_matvec")
     return Y, V
 
 
