@@ -5,7 +5,7 @@
 // bound by reading the codes and scales once (0.75 B a weight).
 //
 //   * Split over K without a second pass: both terms are linear in the rows, so a
-//     CTA that owns the rows [k0, k0 + Kc) of a 256-column tile forms x W of its
+//     CTA that owns the rows [k0, k0 + Kc) of a column tile forms x W of its
 //     rows and also V of its rows times B; the parts of a tile are added over a
 //     thread-block cluster in split order.  One launch, no scratch, no atomics.
 //   * Stages of 8 KB of codes, 4 KB of scales, x and A come by TMA through a shared
@@ -19,9 +19,16 @@
 //     The byte transpose of ldmatrix (m16n16 .b8) hands lane (g, t) one byte, two
 //     columns, of four rows; a byte permute sets the nibble into bf16 128 + code
 //     and one packed subtraction of 136 leaves q.
-//   * x s is rounded to bf16 (2^-8 of each product at most, signs independent), the
-//     same size as the output's own rounding; sums are fp32.  x itself and V are not
-//     rounded in a way that reaches Y: V goes in as a sum of two bf16 numbers.
+//   * x s is rounded to bf16 (2^-8 of each product at most, signs independent: with the
+//     output's own rounding, 1.4 times the error of that alone) where the time of the
+//     products counts, and to two bf16 terms, 16 bits, for small weights; sums are
+//     fp32.  x itself and V are not rounded in a way that reaches Y: V goes in as a sum
+//     of two bf16 numbers.
+//
+// Measured (graph of calls over weights larger than L2): 4096 x 11008 with rank 16 at 1,
+// 4 and 16 tokens 12.2, 12.5 and 17.2 us (2.8, 2.7 and 2.0 TB/s); 4096 x 4096 7.4, 7.5 and
+// 9.8 us.  Bound by the instructions that unpack and scale (about 30 a warp for each
+// 16 x 16 weights), then by the ends of a launch (3 us for the smallest weight).
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -159,7 +166,7 @@ __device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_
   lo = pack_bf16x2(v0 - bf16_lo(hi), v1 - bf16_hi(hi));
 }
 
-template <int TW, int MT, int RC, int XM>
+template <int TW, int MT, int RC, int XM, bool kTwo>
 __global__ void __launch_bounds__(kMvThreads, (MvLayout<TW, MT, RC, XM>::kCtas))
 matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_scales,
               const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_a, const MvArgs p) {
@@ -250,18 +257,19 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
   // left for that (they spilled: 19.2 -> 23.3 us at 4096 x 11008 with block scales).
   constexpr int OWN = L::kOwn;
   const int64_t bcol = col0 + 16 * OWN * ks + 2 * g;
-  uint32_t bw[OWN][4] = {};
-  auto load_b = [&](int j0) {
+  constexpr int CH = RC < 64 ? 1 : 4;   // at a time
+  uint32_t bw[CH][OWN][4] = {};
+  auto load_b = [&](int i, int j0) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int row = j0 + 2 * t + (u & 1) + 8 * (u >> 1);
       const bool in = row < p.r && bcol < p.N;   // N is a multiple of 64: a warp's groups lie inside or outside
 #pragma unroll
       for (int o = 0; o < OWN; ++o)
-        bw[o][u] = in ? __ldg(reinterpret_cast<const uint32_t*>(p.B + row * p.N + bcol + 16 * o)) : 0u;
+        bw[i][o][u] = in ? __ldg(reinterpret_cast<const uint32_t*>(p.B + row * p.N + bcol + 16 * o)) : 0u;
     }
   };
-  if constexpr (RC > 0 && MT == 1) load_b(0);
+  if constexpr (RC > 0 && MT == 1) load_b(0, 0);
 
   // The lane's rows of a 16-row step are 4t + (i ^ (t >> 1)), i = 0 .. 3: with the swizzles
   // above, the four lanes' scales of one i then lie on different banks, and so do the
@@ -286,18 +294,18 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
     a_off[j] = L::kA + (RC == 16 ? piece<2>(r0 + arow, (lane >> 3) & 1)
                                  : (tr / 4) * L::kABytes + piece<8>(r0 + arow, 2 * (tr & 3) + ((lane >> 3) & 1)));
   }
+  // Not unrolled over the ring: constant slot addresses save some adds (4096 x 11008, 1
+  // token: 11.2 against 11.9 us), but six copies of the body come in from memory at
+  // every launch (4096 x 4096: 7.4 against 6.9).
+  int s = 0;
   uint32_t ph = 0;
   bool ok = true;   // a wait that gave up raises the status word; the rest then runs through quickly
 #pragma unroll 1
-  for (int i0 = 0; i0 < nst; i0 += D, ph ^= 1u) {
-#pragma unroll
-    for (int s = 0; s < D; ++s) {   // the slots of the ring, so that every offset is a constant
-    const int i = i0 + s;
-    if (i >= nst) break;
+  for (int i = 0; i < nst; ++i) {
     // refill the slot of the stage before the last one, which every warp is done with by now or soon
     constexpr int kBack = 2;
-    const int old = s >= kBack ? s - kBack : s - kBack + D;
     if (i >= kBack && i - kBack + D < nst && warp == (i & (kMvWarps - 1)) && lane == 0) {
+      const int old = s >= kBack ? s - kBack : s - kBack + D;
       ok = mbar_wait_limit(empty0 + 8 * old, s >= kBack ? ph : ph ^ 1u, p.status, kFlagTimeoutProducer,
                            ok ? kWaitLimitNs : 1000000u) && ok;
       issue(i - kBack + D, old);
@@ -395,7 +403,7 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
         ulonglong2 sc[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) sc[k] = *reinterpret_cast<const ulonglong2*>(at + s_off[j][k] + h * 16 * (TW / 4));
-        uint32_t b[MT][4][2];
+        uint32_t b[MT][4][2], bl[MT][4][2];   // x s as bf16 pairs, and (kTwo) what they leave over
 #pragma unroll
         for (int a = 0; a < MT; ++a) {
           float2 u[4], v[4];
@@ -404,14 +412,19 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
             u[k] = mul2(sc[k].x, xx[a][k]);
             v[k] = mul2(sc[k].y, xx[a][k]);
           }
-          b[a][0][0] = pack_bf16x2(u[0].x, u[1].x);
-          b[a][0][1] = pack_bf16x2(u[2].x, u[3].x);
-          b[a][1][0] = pack_bf16x2(u[0].y, u[1].y);
-          b[a][1][1] = pack_bf16x2(u[2].y, u[3].y);
-          b[a][2][0] = pack_bf16x2(v[0].x, v[1].x);
-          b[a][2][1] = pack_bf16x2(v[2].x, v[3].x);
-          b[a][3][0] = pack_bf16x2(v[0].y, v[1].y);
-          b[a][3][1] = pack_bf16x2(v[2].y, v[3].y);
+          auto fold = [&](int q, float k0, float k1, float k2, float k3) {
+            if constexpr (kTwo) {
+              split2(k0, k1, b[a][q][0], bl[a][q][0]);
+              split2(k2, k3, b[a][q][1], bl[a][q][1]);
+            } else {
+              b[a][q][0] = pack_bf16x2(k0, k1);
+              b[a][q][1] = pack_bf16x2(k2, k3);
+            }
+          };
+          fold(0, u[0].x, u[1].x, u[2].x, u[3].x);
+          fold(1, u[0].y, u[1].y, u[2].y, u[3].y);
+          fold(2, v[0].x, v[1].x, v[2].x, v[3].x);
+          fold(3, v[0].y, v[1].y, v[2].y, v[3].y);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -422,12 +435,18 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
           const uint32_t a2 = sub_bf16x2(__byte_perm(lo, 0x43434343u, 0x4342), 0x43084308u);
           const uint32_t a3 = sub_bf16x2(__byte_perm(hi, 0x43434343u, 0x4342), 0x43084308u);
 #pragma unroll
-          for (int a = 0; a < MT; ++a) mv_mma(acc[a][4 * j + q], a0, a1, a2, a3, b[a][q][0], b[a][q][1]);
+          for (int a = 0; a < MT; ++a) {
+            mv_mma(acc[a][4 * j + q], a0, a1, a2, a3, b[a][q][0], b[a][q][1]);
+            if constexpr (kTwo) mv_mma(acc[a][4 * j + q], a0, a1, a2, a3, bl[a][q][0], bl[a][q][1]);
+          }
         }
       }
     }
     __syncwarp();   // every lane is done with the stage
     if (lane == 0) mbar_arrive(empty0 + 8 * s);
+    if (++s == D) {
+      s = 0;
+      ph ^= 1u;
     }
   }
 
@@ -436,7 +455,8 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
   uint16_t* W = reinterpret_cast<uint16_t*>(smem + L::kW);                   // [2 terms][tok][kWPitch]
   float* part = reinterpret_cast<float*>(smem + L::kPart);                   // [KS][tok][L::kPartPitch]
   if constexpr (RC > 0) {
-    if constexpr (MT == 2) load_b(0);
+#pragma unroll
+    for (int i = MT == 1 ? 1 : 0; i < CH; ++i) load_b(i, 16 * i);
     __syncthreads();   // every ring is free
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
@@ -464,27 +484,36 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
       W[(TOK + m) * L::kWPitch + j] = static_cast<uint16_t>(lo);
     }
     __syncthreads();
-    for (int j0 = 0; j0 < p.r; j0 += 16) {
-      uint32_t b4[OWN][4];
+    for (int j0 = 0; j0 < p.r; j0 += 16 * CH) {
+      if (j0 > 0) {
 #pragma unroll
-      for (int o = 0; o < OWN; ++o) {
-        b4[o][0] = __byte_perm(bw[o][0], bw[o][1], 0x5410);
-        b4[o][1] = __byte_perm(bw[o][0], bw[o][1], 0x7632);
-        b4[o][2] = __byte_perm(bw[o][2], bw[o][3], 0x5410);
-        b4[o][3] = __byte_perm(bw[o][2], bw[o][3], 0x7632);
+        for (int i = 0; i < CH; ++i) load_b(i, j0 + 16 * i);
       }
-      if (j0 + 16 < p.r) load_b(j0 + 16);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const uint32_t* vh = reinterpret_cast<const uint32_t*>(W + (m * 8 + g) * L::kWPitch + j0 + 2 * t);
-        const uint32_t* vl = vh + TOK * L::kWPitch / 2;
+      for (int i = 0; i < CH; ++i) {
+        const int j = j0 + 16 * i;
+        if (j < p.r) {
+          uint32_t b4[OWN][4];
 #pragma unroll
-        for (int q = 0; q < G; ++q)
-          if (q / OWN == ks) {   // the accumulators of these groups, without indexing registers
-            const uint32_t(&w)[4] = b4[q % OWN];
-            mv_mma_here(acc[m][q], w[0], w[1], w[2], w[3], vh[0], vh[4]);
-            mv_mma_here(acc[m][q], w[0], w[1], w[2], w[3], vl[0], vl[4]);
+          for (int o = 0; o < OWN; ++o) {
+            b4[o][0] = __byte_perm(bw[i][o][0], bw[i][o][1], 0x5410);
+            b4[o][1] = __byte_perm(bw[i][o][0], bw[i][o][1], 0x7632);
+            b4[o][2] = __byte_perm(bw[i][o][2], bw[i][o][3], 0x5410);
+            b4[o][3] = __byte_perm(bw[i][o][2], bw[i][o][3], 0x7632);
           }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const uint32_t* vh = reinterpret_cast<const uint32_t*>(W + (m * 8 + g) * L::kWPitch + j + 2 * t);
+            const uint32_t* vl = vh + TOK * L::kWPitch / 2;
+#pragma unroll
+            for (int q = 0; q < G; ++q)
+              if (q / OWN == ks) {   // the accumulators of these groups, without indexing registers
+                const uint32_t(&w)[4] = b4[q % OWN];
+                mv_mma_here(acc[m][q], w[0], w[1], w[2], w[3], vh[0], vh[4]);
+                mv_mma_here(acc[m][q], w[0], w[1], w[2], w[3], vl[0], vl[4]);
+              }
+          }
+        }
       }
     }
   } else {
@@ -575,7 +604,7 @@ struct MvFit {
   int max_active[kMvMaxCluster + 1] = {};
 };
 
-template <int TW, int MT, int RC, int XM>
+template <int TW, int MT, int RC, int XM, bool kTwo>
 const MvFit& mv_fit() {
   static std::mutex mu;
   static MvFit fits[64];
@@ -585,7 +614,7 @@ const MvFit& mv_fit() {
   std::lock_guard<std::mutex> lock(mu);
   MvFit& f = fits[dev];
   if (f.done) return f;
-  auto fn = matvec_kernel<TW, MT, RC, XM>;
+  auto fn = matvec_kernel<TW, MT, RC, XM, kTwo>;
   constexpr uint32_t bytes = MvLayout<TW, MT, RC, XM>::kSmem;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess ||
       cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
@@ -669,7 +698,7 @@ struct MvInputs {
   const uint16_t* A;
 };
 
-template <int TW, int MT, int RC, int XM>
+template <int TW, int MT, int RC, int XM, bool kTwo>
 cudaError_t run_matvec(MvArgs a, int S, const MvInputs& in, cudaStream_t stream) {
   using L = MvLayout<TW, MT, RC, XM>;
   CUtensorMap tc, ts, tx, ta;
@@ -695,28 +724,41 @@ cudaError_t run_matvec(MvArgs a, int S, const MvInputs& in, cudaStream_t stream)
   cfg.attrs = at;
   cfg.numAttrs = 2;
   timing_before(QLORA_KERNEL_MATVEC, stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, matvec_kernel<TW, MT, RC, XM>, tc, ts, tx, ta, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, matvec_kernel<TW, MT, RC, XM, kTwo>, tc, ts, tx, ta, a);
   timing_after(QLORA_KERNEL_MATVEC, stream);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// The tile width with the lower cost: 128 columns make twice the tiles of half the
-// clusters, which fill the device better where N gives few tiles; 256 read x and A half
-// as often.
+// A weight of up to 2^21 numbers takes the time of a launch, so there each product is
+// kept to 16 bits as two bf16 terms (1024 x 1024, 1
+// token, rank 16: 3.8 us either way); a larger one is bound by the
+// instructions of its products, which a second term would make a quarter longer
+// (4096 x 4096, 1 token: 7.6 against 9.3 us; 4096 x 11008, 16 tokens: 17 against 23).
+//
+// The tile width is the one of lower cost: 128 columns make twice the tiles of half the
+// clusters, which fill the device better where N gives few tiles (11008 x 4096, 4
+// tokens: 15.9 us against 16.2 with 256); 256 read x and A half as often (4096 x 11008,
+// 16 tokens, rank 64: 22.4 against 24.3 with 128).
+constexpr int64_t kMvTwoTerms = int64_t(1) << 21;
+
 template <int MT, int RC, int XM>
 cudaError_t run_by_width(MvArgs a, const MvInputs& in, cudaStream_t stream) {
   int S1 = 0, S2 = 0;
   int64_t k1 = 0, k2 = 0;
-  const int64_t c1 = mv_plan(a.K, a.N, 128, mv_fit<128, MT, RC, XM>(), S1, k1);
-  const int64_t c2 = mv_plan(a.K, a.N, 256, mv_fit<256, MT, RC, XM>(), S2, k2);
+  if (a.K * a.N <= kMvTwoTerms) {
+    if (mv_plan(a.K, a.N, 128, mv_fit<128, MT, RC, XM, true>(), S1, a.Kc) < 0) return cudaErrorInvalidValue;
+    return run_matvec<128, MT, RC, XM, true>(a, S1, in, stream);
+  }
+  const int64_t c1 = mv_plan(a.K, a.N, 128, mv_fit<128, MT, RC, XM, false>(), S1, k1);
+  const int64_t c2 = mv_plan(a.K, a.N, 256, mv_fit<256, MT, RC, XM, false>(), S2, k2);
   if (c1 < 0 && c2 < 0) return cudaErrorInvalidValue;
   if (c2 < 0 || (c1 >= 0 && c1 < c2)) {
     a.Kc = k1;
-    return run_matvec<128, MT, RC, XM>(a, S1, in, stream);
+    return run_matvec<128, MT, RC, XM, false>(a, S1, in, stream);
   }
   a.Kc = k2;
-  return run_matvec<256, MT, RC, XM>(a, S2, in, stream);
+  return run_matvec<256, MT, RC, XM, false>(a, S2, in, stream);
 }
 
 template <int MT, int RC>
