@@ -687,35 +687,6 @@ def time_int16_rows(wl, pk):
     return out
 
 
-def graph_per_call(fn, iters):
-    """Device time (ms) per call of fn(0 .. iters - 1) captured in one CUDA graph,
-    median of five replays."""
-    import torch
-    for i in range(3):
-        fn(i)
-    torch.cuda.synchronize()
-    graph = torch.cuda.CUDAGraph()
-    side = torch.cuda.Stream()
-    side.wait_stream(torch.cuda.current_stream())
-    with torch.cuda.stream(side):
-        with torch.cuda.graph(graph, stream=side):
-            for i in range(iters):
-                fn(i)
-    torch.cuda.current_stream().wait_stream(side)
-    graph.replay()
-    torch.cuda.synchronize()
-    times = []
-    for _ in range(5):
-        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-        e0.record()
-        graph.replay()
-        e1.record()
-        torch.cuda.synchronize()
-        times.append(e0.elapsed_time(e1) / iters)
-    del graph
-    return statistics.median(times)
-
-
 def time_block_rows(pk):
     """What stands around the layer: the residual addition with RMS norm and its
     gradient at 2048 and 8192 tokens of 4096 (the larger under dropout), and the

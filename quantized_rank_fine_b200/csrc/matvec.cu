@@ -27,8 +27,10 @@
 //
 // Measured (graph of calls over weights larger than L2): 4096 x 11008 with rank 16 at 1,
 // 4 and 16 tokens 12.2, 12.5 and 17.2 us (2.8, 2.7 and 2.0 TB/s); 4096 x 4096 7.4, 7.5 and
-// 9.8 us.  Bound by the instructions that unpack and scale (about 30 a warp for each
-// 16 x 16 weights), then by the ends of a launch (3 us for the smallest weight).
+// 9.8 us.  36 warp-instructions for each 16 x 16 weights at 1 token, 51 at 16 (whole launch):
+// 52% of the cycles issue one and DRAM runs at 26 and 20% of its peak, so it is bound by
+// unpacking and scaling with 16 warps an SM, then by the ends of a launch (3 us for the
+// smallest weight).
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -295,8 +297,8 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
                                  : (tr / 4) * L::kABytes + piece<8>(r0 + arow, 2 * (tr & 3) + ((lane >> 3) & 1)));
   }
   // Not unrolled over the ring: constant slot addresses save some adds (4096 x 11008, 1
-  // token: 11.2 against 11.9 us), but six copies of the body come in from memory at
-  // every launch (4096 x 4096: 7.4 against 6.9).
+  // token, no adapter: 11.2 against 11.7 us), but six copies of the body come in from
+  // memory at every launch (4096 x 4096: 6.9 against 5.9).
   int s = 0;
   uint32_t ph = 0;
   bool ok = true;   // a wait that gave up raises the status word; the rest then runs through quickly
@@ -731,15 +733,15 @@ cudaError_t run_matvec(MvArgs a, int S, const MvInputs& in, cudaStream_t stream)
 }
 
 // A weight of up to 2^21 numbers takes the time of a launch, so there each product is
-// kept to 16 bits as two bf16 terms (1024 x 1024, 1
-// token, rank 16: 3.8 us either way); a larger one is bound by the
-// instructions of its products, which a second term would make a quarter longer
+// kept to 16 bits as two bf16 terms (1024 x 1024, 1 token,
+// rank 16: 3.8 us either way); a larger one is bound by the instructions of its products,
+// which a second term would make a quarter longer
 // (4096 x 4096, 1 token: 7.6 against 9.3 us; 4096 x 11008, 16 tokens: 17 against 23).
 //
 // The tile width is the one of lower cost: 128 columns make twice the tiles of half the
 // clusters, which fill the device better where N gives few tiles (11008 x 4096, 4
-// tokens: 15.9 us against 16.2 with 256); 256 read x and A half as often (4096 x 11008,
-// 16 tokens, rank 64: 22.4 against 24.3 with 128).
+// tokens, rank 16: 15.8 us against 17.3 with 256); 256 read x and A half as often (4096 x
+// 11008, 16 tokens, rank 64: 20.5 against 21.8 with 128).
 constexpr int64_t kMvTwoTerms = int64_t(1) << 21;
 
 template <int MT, int RC, int XM>

@@ -15,10 +15,10 @@
 // the CTAs are added by a second, programmatically dependent launch.
 //
 // Measured (graph of calls over rows larger than L2): forward 2048 x 4096 12.8 us (5.2
-// TB/s of 8 bytes an element); gradient 8192 x 4096 43.8 us (6.1 TB/s) and 4.5 more
-// with the gain's.  Dropout adds Philox's 40 instructions for four elements and makes
-// the instruction rate the bound: forward 8192 x 4096 51 us, with bf16 and 8-bit
-// output 65; gradient 69 us.
+// TB/s of 8 bytes an element); gradient 8192 x 4096 43.6 us (6.2 TB/s) and 4.7 more
+// with the gain's.  Dropout adds Philox's ten rounds for four elements: forward
+// 8192 x 4096 51 us, with bf16 and 8-bit output 66, gradient 69 with the gain's; then 71
+// and 62% of the cycles issue an instruction and DRAM runs at 51 and 55% of its peak.
 #include "common.cuh"
 #include "kernels.h"
 #include "philox.cuh"
