@@ -190,6 +190,7 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
   const int nst = static_cast<int>(((p.K - kbeg < p.Kc ? p.K - kbeg : p.Kc) + L::kRows - 1) / L::kRows);
   const int64_t col0 = static_cast<int64_t>(tile) * TW + cg * L::kCols;   // first column of this warp
 
+  cluster_started_arrive();
   if (tid == 0) {
     for (int s = 0; s < D; ++s) {
       mbar_init(full0 + 8 * s, 1);
@@ -544,6 +545,7 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
   const int groups = gy + (RC > 0 && tile == 0 && p.V ? p.M * p.r / 4 : 0);
   const int cap = (groups + S - 1) / S;
   const uint32_t recv_addr = smem_addr(recv);
+  cluster_started_wait();
   for (int q = tid; q < groups; q += kMvThreads) {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (q < gy) {
@@ -662,15 +664,13 @@ int64_t mv_plan(int64_t K, int64_t N, int tw, const MvFit& fit, int& S, int64_t&
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 mv_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {   // looked up once, whichever threads call first
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(
+        e == cudaSuccess && q == cudaDriverEntryPointSuccess ? ptr : nullptr);
+  }();
   return fn;
 }
 

@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_bwd_kernel(const __gr
                                                                       const int threads, const int groups) {
   __shared__ float red[2][kCluster ? 32 * kBwdMaxCluster : 32];
   __shared__ float4 sums[kCluster ? 1 : kBwdThreads * 2];
+  if constexpr (kCluster) cluster_started_arrive();
   grid_launch_dependents();
   grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = threads >> 5;
@@ -362,6 +363,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_bwd_kernel(const __gr
   if (mine) load_gain(p.G, p.g_f32, v, g);
   int flip = 0;
   load(first + group);
+  if constexpr (kCluster) cluster_started_wait();
   for (int64_t r0 = first; r0 < p.M; r0 += step, flip ^= 1) {   // the same turns for every thread
     const int64_t row = r0 + group;
     const float rs = rstd;
