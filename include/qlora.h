@@ -469,8 +469,9 @@ QLORA_API qlora_status qlora_loftq_split(const float* U, int64_t ldu, const floa
  *   Q        [device] out: y in 8 bits, uint8 (M, n) E4M3 codes, or NULL.  Per block
  *            of q_block columns (64, or 0 for the whole row): a = max |y|,
  *            s = fl32(a / 448) (0 where that is below 2^-126), code =
- *            E4M3(fl32(y / s)) round to nearest even (0 where s = 0), so y ~ code s.  y is not rounded to bf16 in between.  A block that holds a
- *            NaN or an infinity gets codes and a scale whose products are NaN.
+ *            E4M3(fl32(y / s)) round to nearest even (0 where s = 0), so y ~ code s.
+ *            y is not rounded to bf16 in between.  A block that holds a NaN or an
+ *            infinity gets codes and a scale whose products are NaN.
  *   q_scales [device] out: fp32 (M, n / 64), or (M) with q_block = 0.  With Q only.
  *   rstd     [device] out: fp32 (M), for the backward, or NULL.
  * QLORA_ERR_INVALID_ARG without Y and Q, with Q but no q_scales, or for another q_block.
@@ -514,7 +515,9 @@ QLORA_API size_t qlora_rmsnorm_ws_bytes(int64_t M, int64_t n);
  *   Y = bf16(X w' + s (X A) B),   V = bf16(s X A),   w' = (code - 8) scale
  * with fp32 accumulation.  Unlike qlora_linear_fwd it does not round w' or the V in
  * Y to bf16 (it rounds the products x scale instead, once, to bf16), and it reads
- * 8-bit activations as qlora_rmsnorm_fwd writes them.
+ * 8-bit activations as qlora_rmsnorm_fwd writes them.  What an infinity or a NaN
+ * reaches is not finite, but an infinity may come out as NaN (numbers are carried as
+ * the sum of two in places).
  *   w         [host] descriptor; another format is QLORA_ERR_INVALID_ARG.
  *   X         [device] bf16 (M, in), or with x_scales uint8 (M, in) E4M3 codes.
  *   x_scales  [device] fp32 (M, in / 64) for x_block = 64, (M) for x_block = 0:

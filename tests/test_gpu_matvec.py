@@ -143,6 +143,30 @@ def test_nan_stays_in_its_row():
     assert torch.equal(Y[rows], Y0[rows]) and torch.equal(V[rows], V0[rows])
 
 
+@pytest.mark.parametrize("K,N", [(256, 192), (2048, 1536)])
+@pytest.mark.parametrize("x8", [None, 0, 64])
+def test_infinities_stay_visible(K, N, x8):
+    """An infinity in A, in B or in a scale of the weight: what it reaches is not
+    finite, and every other output keeps its bits."""
+    w, X, x64, A, B, w64 = _case(5, K, N, 16, x8, 21)
+    Y0, V0 = q.qlora_matvec(w, X, q.Workspace(), A, B, save_V=True)
+    A2 = A.clone()
+    A2[70, 3] = float("inf")
+    Y, V = q.qlora_matvec(w, X, q.Workspace(), A2, B, save_V=True)
+    assert not torch.isfinite(Y).any() and not torch.isfinite(V[:, 3]).any()
+    keep = [i for i in range(16) if i != 3]
+    assert torch.equal(V[:, keep], V0[:, keep])
+    B2 = B.clone()
+    B2[9, 100] = float("-inf")
+    Y, V = q.qlora_matvec(w, X, q.Workspace(), A, B2, save_V=True)
+    cols = torch.arange(N, device="cuda") != 100
+    assert not torch.isfinite(Y[:, 100]).any() and torch.equal(Y[:, cols], Y0[:, cols]) and torch.equal(V, V0)
+    w.dq_scales.view(K, N // 16)[31, 2] = float("inf")
+    Y, V = q.qlora_matvec(w, X, q.Workspace(), A, B, save_V=True)
+    cols = torch.arange(N, device="cuda") // 16 != 2
+    assert not torch.isfinite(Y[:, 32:48]).any() and torch.equal(Y[:, cols], Y0[:, cols]) and torch.equal(V, V0)
+
+
 def test_matches_the_layer_forward():
     """The layer's forward on the same integer weight multiplies with bf16(w')."""
     w, X, x64, A, B, w64 = _case(8, 1024, 768, 16, None, 2)
@@ -185,6 +209,47 @@ def test_graph_replay_and_chain():
         got.zero_()
         g.replay()
         assert torch.equal(got, want)
+
+
+def test_first_call_of_a_variant_inside_a_capture():
+    """A variant that no call has prepared yet (120 adapter columns, row scales) is
+    captured at once; the replay has the bits of a call made after it."""
+    for K, N in ((512, 256), (2048, 1536)):
+        w, X, x64, A, B, w64 = _case(13, K, N, 120, 0, 31)
+        ws = q.Workspace()
+        ws.get(1 << 16)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            Y, V = q.qlora_matvec(w, X, ws, A, B, save_V=True)
+        g.replay()
+        torch.cuda.synchronize()
+        _check(Y, V, x64, A, B, w64)
+        want = q.qlora_matvec(w, X, ws, A, B, save_V=True)
+        assert torch.equal(Y, want[0]) and torch.equal(V, want[1])
+
+
+def test_two_host_threads():
+    """Calls from two threads at once, each on a stream and a workspace of its own."""
+    import threading
+    w, X, x64, A, B, w64 = _case(6, 1024, 768, 16, 64, 33)
+    want, _ = q.qlora_matvec(w, X, q.Workspace(), A, B)
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def work(i):
+        st, ws = torch.cuda.Stream(), q.Workspace()
+        with torch.cuda.stream(st):
+            ys = [q.qlora_matvec(w, X, ws, A, B)[0] for _ in range(50)]
+        st.synchronize()
+        got[i] = ys
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(torch.equal(y, want) for ys in got for y in ys)
 
 
 def test_fresh_weights_each_call():
