@@ -2,10 +2,12 @@
 in-place residual streams, calls of one workspace that outgrow it under a captured
 graph, mixed chains of the library's dependent launches, kernel timers."""
 
+import numpy as np
 import pytest
 import torch
 
 import quantized_rank_fine_b200 as q
+from oracle import norm
 from tests.helpers import layer_on_gpu, require_gpu
 
 pytestmark = pytest.mark.gpu
@@ -163,3 +165,29 @@ def test_kernel_timers_and_launch_count():
         torch.cuda.synchronize()
         assert all(0 < t < 50 for t in tm.times_ms())
         tm.disarm()
+
+
+def test_norms_past_32_bit_offsets():
+    """More than 2^31 elements: the last rows are where 64-bit offsets put them, and
+    their masks count elements in 64 bits."""
+    n, M = 65536, 32776
+    x = torch.zeros((M, n), dtype=BF, device="cuda")
+    last = _rn(2, n, seed=3).to(BF)
+    x[-2:] = last
+    g = _rn(n, seed=4)
+    d = q.Dropout(0.25, 7, 9)
+    s = norm.keep_scale(0.25)
+    keep = torch.from_numpy(norm.words(7, 9, (M - 2) * n, 2 * n).reshape(2, n) >= np.uint32(2 ** 30)).cuda()
+    o = q.qlora_rmsnorm_fwd(x, g, 1e-5, dropout=d, save_rstd=True)
+    h = torch.where(keep, last.double() * s, 0.0).to(BF)
+    assert torch.equal(o.H[-2:], h) and torch.count_nonzero(o.H[:-2]) == 0
+    a = q.qlora_rmsnorm_fwd(h, g, 1e-5, save_rstd=True)
+    assert torch.equal(o.Y[-2:], a.Y) and torch.equal(o.rstd[-2:], a.rstd) and torch.count_nonzero(o.Y[:-2]) == 0
+    dX, dR, _ = q.qlora_rmsnorm_bwd(x, o.H, g, o.rstd, q.Workspace(), dropout=d, need_dG=False, dR=o.Y)
+    want = q.qlora_rmsnorm_bwd(last, h, g, a.rstd, q.Workspace(), need_dG=False)[1]
+    assert torch.equal(dR[-2:], want) and torch.count_nonzero(dX[:-2]) == 0 and torch.count_nonzero(dX[-2:][~keep]) == 0
+    # dX is the rounding of the unrounded gradient times s: two roundings of half a step
+    ref = torch.where(keep, want.double() * s, 0.0)
+    assert ((dX[-2:].double() - ref).abs() <= 2.0 ** -7 * 1.01 * ref.abs()).all()
+    del x, o, dX, dR
+    torch.cuda.empty_cache()
