@@ -26,9 +26,9 @@
 //     of two bf16 numbers.
 //
 // Measured (graph of calls over weights larger than L2): 4096 x 11008 with rank 16 at 1,
-// 4 and 16 tokens 12.2, 12.5 and 17.2 us (2.8, 2.7 and 2.0 TB/s); 4096 x 4096 7.4, 7.5 and
-// 9.8 us.  36 warp-instructions for each 16 x 16 weights at 1 token, 51 at 16 (whole launch):
-// 52% of the cycles issue one and DRAM runs at 26 and 20% of its peak, so it is bound by
+// 4 and 16 tokens 12.3, 12.7 and 17.2 us (2.8, 2.7 and 2.0 TB/s); 4096 x 4096 7.3, 7.6 and
+// 10.1 us.  36 warp-instructions for each 16 x 16 weights at 1 token, 51 at 16 (whole launch):
+// 52% of the cycles issue one and DRAM runs at 27 and 20% of its peak, so it is bound by
 // unpacking and scaling with 16 warps an SM, then by the ends of a launch (3 us for the
 // smallest weight).
 #include "common.cuh"
