@@ -141,6 +141,7 @@ nf4_gemv_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_const
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
+  cluster_started_arrive();
   grid_launch_dependents();
   const int tile = blockIdx.x, split = blockIdx.y;
   const int64_t k_begin = static_cast<int64_t>(split) * p.Kc;
@@ -407,6 +408,7 @@ nf4_gemv_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_const
   const int groups = p.M * (kTileCols / 4);
   const int cap = (groups + S - 1) / S;
   const uint32_t recv_addr = smem_addr(recv);
+  cluster_started_wait();   // every peer's shared memory may be written
   for (int q = tid; q < groups; q += kGvThreads) {
     const int o = q / cap, slot = q - o * cap;
     const float4 v = *reinterpret_cast<const float4*>(part + 4 * q);

@@ -143,6 +143,7 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constan
   const uint32_t full0 = smem_addr(bars), free0 = smem_addr(bars + kSkStages);
   const uint32_t tmem_full = smem_addr(bars + 2 * kSkStages);
 
+  cluster_started_arrive();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row0 = static_cast<int64_t>(second ? static_cast<int>(blockIdx.x) - rt0 : blockIdx.x) * kRowsT;
   const int split = blockIdx.y;
@@ -180,6 +181,9 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constan
   // before; nothing in global memory is touched until that kernel has finished.
   grid_dependency_wait();
   grid_launch_dependents();
+  // A split with an empty slice reaches its stores at once: before the roles part,
+  // every CTA of the cluster has started, so its shared memory may be written.
+  cluster_started_wait();
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer

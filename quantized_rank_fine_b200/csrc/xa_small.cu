@@ -53,6 +53,7 @@ struct XaArgs {
 };
 
 __global__ void __launch_bounds__(kXaThreads) xa_small_kernel(const XaArgs p) {
+  cluster_started_arrive();
   // Everything before this kernel has finished once the wait returns, so the
   // dependent launched right after (which reads its own inputs at once) sees
   // them complete.
@@ -145,6 +146,7 @@ __global__ void __launch_bounds__(kXaThreads) xa_small_kernel(const XaArgs p) {
   const int E = p.M * cols;
   const int cap = (E + S - 1) / S;
   const uint32_t recv_addr = smem_addr(recv);
+  cluster_started_wait();   // every peer's shared memory may be written
   for (int e = tid; e < E; e += kXaThreads) {
     const int o = e / cap, slot = e - o * cap;
     st_shared_cluster_f32(mapa_shared(recv_addr + static_cast<uint32_t>((rank * cap + slot) * 4), o), part[e]);
