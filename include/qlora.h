@@ -511,10 +511,12 @@ QLORA_API size_t qlora_rmsnorm_ws_bytes(int64_t M, int64_t n);
 /*
  * A few tokens through an integer weight (dq_format QLORA_FMT_INT16: 4-bit codes,
  * one scale per 16 weights), with or without adapters -- the decode step of a
- * layer on that base, at the speed of reading the weight once:
+ * layer on that base, in one launch that reads the weight once:
  *   Y = bf16(X w' + s (X A) B),   V = bf16(s X A),   w' = (code - 8) scale
  * with fp32 accumulation.  Unlike qlora_linear_fwd it does not round w' or the V in
- * Y to bf16 (it rounds the products x scale instead, once, to bf16), and it reads
+ * Y to bf16: x scale and V enter the products with 16 bits (as the sum of two bf16
+ * numbers), at every size, so before its own rounding Y is within about 2^-14 of the
+ * root of the sum of its squared products x w', also where they cancel.  It reads
  * 8-bit activations as qlora_rmsnorm_fwd writes them.  What an infinity or a NaN
  * reaches is not finite, but an infinity may come out as NaN (numbers are carried as
  * the sum of two in places).

@@ -2,7 +2,8 @@
 //
 //   Y[m][n] = sum_k x[m][k] q[k][n] s[k][n / 16] + sum_j V[m][j] B[j][n],  V = scale X A
 //
-// bound by reading the codes and scales once (0.75 B a weight).
+// Its floor is to read the codes and scales once (0.75 B a weight); what it is bound by
+// is below.
 //
 //   * Split over K without a second pass: both terms are linear in the rows, so a
 //     CTA that owns the rows [k0, k0 + Kc) of a column tile forms x W of its
@@ -15,22 +16,23 @@
 //   * Tensor cores with the weight as the 16 x 16 A operand and 8 tokens as the B
 //     operand: mma.sync m16n8k16 (128-row tcgen05 tiles have no use for 16 tokens).
 //     The 16 operand rows are the 16 columns that share a scale, so the scale
-//     folds into x: B = bf16(x s), and A is the integer q itself, exact in bf16.
+//     folds into x: B = x s, and A is the integer q itself, exact in bf16.
 //     The byte transpose of ldmatrix (m16n16 .b8) hands lane (g, t) one byte, two
 //     columns, of four rows; a byte permute sets the nibble into bf16 128 + code
 //     and one packed subtraction of 136 leaves q.
-//   * x s is rounded to bf16 (2^-8 of each product at most, signs independent: with the
-//     output's own rounding, 1.4 times the error of that alone) where the time of the
-//     products counts, and to two bf16 terms, 16 bits, for small weights; sums are
-//     fp32.  x itself and V are not rounded in a way that reaches Y: V goes in as a sum
-//     of two bf16 numbers.
+//   * x s goes in as two bf16 terms, bf16(x s) and bf16 of what that leaves: 16 bits, so a
+//     product is within 2^-16 of itself and the output's own rounding decides the error,
+//     at every size of the weight.  (One term is within 2^-8: the relative error against
+//     64 bits is then 0.0024 instead of 0.0017, an output formed by cancellation is off by
+//     2^-8 of its products, and the time 12 to 30% less: 4096 x 4096, rank 16, 1 token
+//     7.1 against 7.9 us, 4096 x 11008, 16 tokens 17.5 against 24.0.  TF32 products, 11
+//     bits, take the time of two bf16 terms.)  V, too, is a sum of two bf16 numbers; sums
+//     are fp32.
 //
 // Measured (graph of calls over weights larger than L2): 4096 x 11008 with rank 16 at 1,
-// 4 and 16 tokens 12.3, 12.7 and 17.2 us (2.8, 2.7 and 2.0 TB/s); 4096 x 4096 7.3, 7.6 and
-// 10.1 us.  36 warp-instructions for each 16 x 16 weights at 1 token, 51 at 16 (whole launch):
-// 52% of the cycles issue one and DRAM runs at 27 and 20% of its peak, so it is bound by
-// unpacking and scaling with 16 warps an SM, then by the ends of a launch (3 us for the
-// smallest weight).
+// 8 and 16 tokens 16.2, 16.5 and 24.0 us (2.1, 2.1 and 1.5 TB/s); 4096 x 4096 7.9, 8.4 and
+// 11.6 us.  Bound by the instructions that unpack, scale and split with 16 warps an SM,
+// then by the ends of a launch (3 us for the smallest weight), not by memory.
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -168,7 +170,7 @@ __device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_
   lo = pack_bf16x2(v0 - bf16_lo(hi), v1 - bf16_hi(hi));
 }
 
-template <int TW, int MT, int RC, int XM, bool kTwo>
+template <int TW, int MT, int RC, int XM>
 __global__ void __launch_bounds__(kMvThreads, (MvLayout<TW, MT, RC, XM>::kCtas))
 matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_scales,
               const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_a, const MvArgs p) {
@@ -242,7 +244,7 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
   // The scales of x and B may have been written by the kernel in front while this one
   // was already resident, so they are read by ordinary loads behind the wait, never by
   // the read-only path.  (Past L1 the block scales, eight blocks of a token to a sector,
-  // come from L2 at every stage: 4096 x 11008, 4 tokens 22.3 us against 14.9.)
+  // come from L2 at every stage: 4096 x 11008, rank 16, 4 tokens 23.9 us against 18.1.)
   //
   // Scales of 8-bit x.  One a row: the loop multiplies with the codes alone, exact in
   // bf16, and the finished sums are scaled.  One per 64 rows: those of tokens g and
@@ -411,7 +413,7 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
         ulonglong2 sc[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) sc[k] = *reinterpret_cast<const ulonglong2*>(at + s_off[j][k] + h * 16 * (TW / 4));
-        uint32_t b[MT][4][2], bl[MT][4][2];   // x s as bf16 pairs, and (kTwo) what they leave over
+        uint32_t b[MT][4][2], bl[MT][4][2];   // x s as bf16 pairs, and what they leave over
 #pragma unroll
         for (int a = 0; a < MT; ++a) {
           float2 u[4], v[4];
@@ -421,13 +423,8 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
             v[k] = mul2(sc[k].y, xx[a][k]);
           }
           auto fold = [&](int q, float k0, float k1, float k2, float k3) {
-            if constexpr (kTwo) {
-              split2(k0, k1, b[a][q][0], bl[a][q][0]);
-              split2(k2, k3, b[a][q][1], bl[a][q][1]);
-            } else {
-              b[a][q][0] = pack_bf16x2(k0, k1);
-              b[a][q][1] = pack_bf16x2(k2, k3);
-            }
+            split2(k0, k1, b[a][q][0], bl[a][q][0]);
+            split2(k2, k3, b[a][q][1], bl[a][q][1]);
           };
           fold(0, u[0].x, u[1].x, u[2].x, u[3].x);
           fold(1, u[0].y, u[1].y, u[2].y, u[3].y);
@@ -445,7 +442,7 @@ matvec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
 #pragma unroll
           for (int a = 0; a < MT; ++a) {
             mv_mma(acc[a][4 * j + q], a0, a1, a2, a3, b[a][q][0], b[a][q][1]);
-            if constexpr (kTwo) mv_mma(acc[a][4 * j + q], a0, a1, a2, a3, bl[a][q][0], bl[a][q][1]);
+            mv_mma(acc[a][4 * j + q], a0, a1, a2, a3, bl[a][q][0], bl[a][q][1]);
           }
         }
       }
@@ -613,7 +610,7 @@ struct MvFit {
   int max_active[kMvMaxCluster + 1] = {};
 };
 
-template <int TW, int MT, int RC, int XM, bool kTwo>
+template <int TW, int MT, int RC, int XM>
 const MvFit& mv_fit() {
   static std::mutex mu;
   static MvFit fits[64];
@@ -623,7 +620,7 @@ const MvFit& mv_fit() {
   std::lock_guard<std::mutex> lock(mu);
   MvFit& f = fits[dev];
   if (f.done) return f;
-  auto fn = matvec_kernel<TW, MT, RC, XM, kTwo>;
+  auto fn = matvec_kernel<TW, MT, RC, XM>;
   constexpr uint32_t bytes = MvLayout<TW, MT, RC, XM>::kSmem;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess ||
       cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
@@ -705,7 +702,7 @@ struct MvInputs {
   const uint16_t* A;
 };
 
-template <int TW, int MT, int RC, int XM, bool kTwo>
+template <int TW, int MT, int RC, int XM>
 cudaError_t run_matvec(MvArgs a, int S, const MvInputs& in, cudaStream_t stream) {
   using L = MvLayout<TW, MT, RC, XM>;
   CUtensorMap tc, ts, tx, ta;
@@ -731,41 +728,33 @@ cudaError_t run_matvec(MvArgs a, int S, const MvInputs& in, cudaStream_t stream)
   cfg.attrs = at;
   cfg.numAttrs = 2;
   timing_before(QLORA_KERNEL_MATVEC, stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, matvec_kernel<TW, MT, RC, XM, kTwo>, tc, ts, tx, ta, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, matvec_kernel<TW, MT, RC, XM>, tc, ts, tx, ta, a);
   timing_after(QLORA_KERNEL_MATVEC, stream);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// A weight of up to 2^21 numbers takes the time of a launch, so there each product is
-// kept to 16 bits as two bf16 terms (1024 x 1024, 1 token,
-// rank 16: 3.8 us either way); a larger one is bound by the instructions of its products,
-// which a second term would make a quarter longer
-// (4096 x 4096, 1 token: 7.6 against 9.3 us; 4096 x 11008, 16 tokens: 17 against 23).
-//
 // The tile width is the one of lower cost: 128 columns make twice the tiles of half the
 // clusters, which fill the device better where N gives few tiles (11008 x 4096, 4
-// tokens, rank 16: 15.8 us against 17.3 with 256); 256 read x and A half as often (4096 x
-// 11008, 16 tokens, rank 64: 20.5 against 21.8 with 128).
-constexpr int64_t kMvTwoTerms = int64_t(1) << 21;
-
+// tokens, rank 16: 15.8 us against 17.3 with 256 before the second term).  On a tie 128
+// columns, whose smaller clusters spread more evenly and end sooner (5120 x 5120, 16
+// tokens, rank 16: 16.7 us against 20.6; 1024 x 1024: 5.2 against 5.6; 4096 x 11008: 24.0
+// against 23.7), but 256 with an adapter of more than 64 columns, which is then read half
+// as often (rank 256, 16 tokens: 512 x 512 14.1 us against 16.9, 5120 x 5120 29.6 against
+// 47.6; rank 64: 7.3 against 7.5 at 1024 x 1024, 24.0 against 19.8 at 5120 x 5120).
 template <int MT, int RC, int XM>
 cudaError_t run_by_width(MvArgs a, const MvInputs& in, cudaStream_t stream) {
   int S1 = 0, S2 = 0;
   int64_t k1 = 0, k2 = 0;
-  if (a.K * a.N <= kMvTwoTerms) {
-    if (mv_plan(a.K, a.N, 128, mv_fit<128, MT, RC, XM, true>(), S1, a.Kc) < 0) return cudaErrorInvalidValue;
-    return run_matvec<128, MT, RC, XM, true>(a, S1, in, stream);
-  }
-  const int64_t c1 = mv_plan(a.K, a.N, 128, mv_fit<128, MT, RC, XM, false>(), S1, k1);
-  const int64_t c2 = mv_plan(a.K, a.N, 256, mv_fit<256, MT, RC, XM, false>(), S2, k2);
+  const int64_t c1 = mv_plan(a.K, a.N, 128, mv_fit<128, MT, RC, XM>(), S1, k1);
+  const int64_t c2 = mv_plan(a.K, a.N, 256, mv_fit<256, MT, RC, XM>(), S2, k2);
   if (c1 < 0 && c2 < 0) return cudaErrorInvalidValue;
-  if (c2 < 0 || (c1 >= 0 && c1 < c2)) {
+  if (c2 < 0 || (c1 >= 0 && (RC > 64 ? c1 < c2 : c1 <= c2))) {
     a.Kc = k1;
-    return run_matvec<128, MT, RC, XM, false>(a, S1, in, stream);
+    return run_matvec<128, MT, RC, XM>(a, S1, in, stream);
   }
   a.Kc = k2;
-  return run_matvec<256, MT, RC, XM, false>(a, S2, in, stream);
+  return run_matvec<256, MT, RC, XM>(a, S2, in, stream);
 }
 
 template <int MT, int RC>
