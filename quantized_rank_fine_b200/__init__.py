@@ -272,7 +272,9 @@ def qlora_workspace_bytes(op: int, M: int, n_in: int, n_out: int, r: int) -> int
 class Workspace:
     """Caller-owned scratch of the forward/backward calls (a device uint8 tensor),
     grown on demand and initialised once through qlora_ws_init.  A buffer that was
-    outgrown is kept: a captured graph or a call in flight may still write to it."""
+    outgrown is kept, since a captured graph or a call in flight may still write to
+    it; each new one is at least half as large again, so the kept ones together are
+    at most twice the newest.  release_outgrown gives them back."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
@@ -281,11 +283,18 @@ class Workspace:
 
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
         if self.buf is None or self.buf.numel() < nbytes:
+            least = 256 if self.buf is None else (3 * self.buf.numel() + 1) // 2
+            buf = torch.empty(max(nbytes, least), dtype=torch.uint8, device=self.device)
+            _check(lib().qlora_ws_init(_ptr(buf), buf.numel(), _stream(stream)), "qlora_ws_init")
             if self.buf is not None:
                 self.outgrown.append(self.buf)
-            self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
-            _check(lib().qlora_ws_init(_ptr(self.buf), self.buf.numel(), _stream(stream)), "qlora_ws_init")
+            self.buf = buf
         return self.buf
+
+    def release_outgrown(self) -> None:
+        """Give back the buffers that were outgrown: for a caller that will replay no
+        graph captured on one and has no call on another stream still using one."""
+        self.outgrown.clear()
 
     def status(self, stream=None) -> int:
         if self.buf is None:
