@@ -292,14 +292,19 @@ class Workspace:
         return self.buf
 
     def release_outgrown(self) -> None:
-        """Give back the buffers that were outgrown: for a caller that will replay no
-        graph captured on one and has no call on another stream still using one."""
+        """Give back the buffers that were outgrown, and with them their status: for a
+        caller that will replay no graph captured on one and has no call on another
+        stream still using one."""
         self.outgrown.clear()
 
     def status(self, stream=None) -> int:
-        if self.buf is None:
-            return 0
-        return lib().qlora_ws_status(_ptr(self.buf), _stream(stream))
+        """qlora_ws_status of this workspace, the buffers it has outgrown and still keeps
+        included: not QLORA_OK if any of them is not (reading clears them all)."""
+        found = 0
+        for buf in (*self.outgrown, self.buf):
+            if buf is not None:
+                found = lib().qlora_ws_status(_ptr(buf), _stream(stream)) or found
+        return found
 
 
 def qlora_quantize_nf4(W0: torch.Tensor, stream=None, out: NF4Weight | None = None,
