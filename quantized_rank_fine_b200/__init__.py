@@ -284,7 +284,9 @@ class Workspace:
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
         if self.buf is None or self.buf.numel() < nbytes:
             least = 256 if self.buf is None else (3 * self.buf.numel() + 1) // 2
-            buf = torch.empty(max(nbytes, least), dtype=torch.uint8, device=self.device)
+            # of the call's stream: memory that the current one has just let go of may still be written
+            with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else _nullcontext():
+                buf = torch.empty(max(nbytes, least), dtype=torch.uint8, device=self.device)
             _check(lib().qlora_ws_init(_ptr(buf), buf.numel(), _stream(stream)), "qlora_ws_init")
             if self.buf is not None:
                 self.outgrown.append(self.buf)

@@ -1,6 +1,8 @@
-"""The binding's Workspace on the device: the status of buffers that it outgrew."""
+"""The binding's Workspace on the device: the status of buffers that it outgrew, and the
+stream that a new one belongs to."""
 
 import pytest
+import torch
 
 import quantized_rank_fine_b200 as q
 from tests.helpers import require_gpu
@@ -35,3 +37,22 @@ def test_timeouts_in_several_buffers_are_read_at_once():
         ws.get(2 * ws.buf.numel())
     assert ws.status() == QLORA_ERR_TIMEOUT
     assert ws.status() == 0
+
+
+def test_new_buffer_belongs_to_the_stream_of_the_call():
+    """A buffer first asked for by a call on another stream is not memory that the current
+    stream, still busy, has only just let go of: it stays zero."""
+    n = 1 << 20
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        old = [torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        torch.cuda._sleep(20_000_000)          # about 10 ms
+        for t in old:
+            t.fill_(0xFF)
+        t = None
+        old.clear()
+        ws = q.Workspace()
+        ws.get(n, side)
+        torch.cuda.synchronize()
+        assert torch.count_nonzero(ws.buf) == 0
