@@ -160,16 +160,25 @@ __device__ __forceinline__ float block_scale(uint32_t top) {
 // theorem (IBM Journal of Research and Development 34, 1990): with the reciprocal r
 // of s, the product q = y r and the rest y - q s, each rounded once, q + (y - q s) r
 // is the correctly rounded quotient, as long as the rest does not underflow (|y|
-// above about 2^-100).
-__device__ __forceinline__ uint2 e4m3_codes(const float (&y)[8], float s) {
+// above about 2^-100).  A block of tiny values is therefore brought up by a power of
+// two, y and s alike; above, a y whose rest underflows is far below the smallest code.
+__device__ __forceinline__ uint2 e4m3_codes(const float (&v)[8], float s) {
   if (s == 0.0f) return make_uint2(0u, 0u);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = v[i];
+  if (s < 0x1p-60f) {
+    s *= 0x1p64f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] *= 0x1p64f;
+  }
   const float inv = __frcp_rn(s);
   const float2 r2 = make_float2(inv, inv), s2 = make_float2(-s, -s);
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 v = make_float2(y[2 * i], y[2 * i + 1]), q0 = mul2(v, r2);
-    const float2 q = fma2(fma2(q0, s2, v), r2, q0);
+    const float2 u = make_float2(y[2 * i], y[2 * i + 1]), q0 = mul2(u, r2);
+    const float2 q = fma2(fma2(q0, s2, u), r2, q0);
     w[i] = e4m3_pair(q.x, q.y);
   }
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
