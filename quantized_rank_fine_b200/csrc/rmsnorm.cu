@@ -7,7 +7,7 @@
 //   gh = g dy,  c = mean(gh h) rstd^2,  dh = rstd (gh - h c) + dH
 //   out: dR = bf16(dh), dX = bf16(keep dh / (1 - p)), dG = sum over rows of dy h rstd
 //
-// Both are bound by streaming the rows once (a few flops and bytes an element).
+// The floor of both is to stream the rows once (a few flops and bytes an element).
 // A CTA takes a row: every thread holds its 16-byte vectors of the row in
 // registers, so the row is read once however many passes the arithmetic takes.
 // The gradient's CTAs walk several rows with the next row's loads in flight, and
@@ -19,6 +19,12 @@
 // with the gain's.  Dropout adds Philox's ten rounds for four elements: forward
 // 8192 x 4096 51 us, with bf16 and 8-bit output 66, gradient 69 with the gain's; then 71
 // and 62% of the cycles issue an instruction and DRAM runs at 51 and 55% of its peak.
+// Not at the floor either: short rows forward, where every row has a CTA of its own
+// (8192 x 512 9.2 us of 5.1, 65536 x 64 68 of 5; the gradient without the gain's,
+// several rows a CTA, 6.9 and 19); rows past 8192 columns, where one CTA of up to 1024
+// threads fits on an SM and nothing covers a row's latency but the next row (2048 x
+// 16384 forward 51 us of 41, gradient 71; 512 x 65536 58 and 134); and the gain's
+// gradient, whose parts pass through memory once more (2048 x 4096 15.9 us, 11.6 without).
 #include "common.cuh"
 #include "kernels.h"
 #include "philox.cuh"
